@@ -350,6 +350,138 @@ dsa_status dsa_verify(const float *p, const float *q, const int32_t *draft, cons
                       int B, int S, int V, float *alpha, int32_t *accept, int32_t *token, int32_t *accepted_len,
                       cudaStream_t stream);
 
+/*
+ * Around the verify step on a serving path: the queries' rotary part (dsa_rope), the new
+ * tokens' rows into a paged cache (dsa_cache_append), the attention of a chunk of new
+ * tokens over it (dsa_paged_attn), and the probabilities that dsa_verify takes
+ * (dsa_logits_probs).  The pages name the parts (a 64-wide rotary part of the 576-wide row,
+ * a paged cache of a serving engine, rejection sampling over the two models'
+ * probabilities) and print no formula; the forms below are the readings implemented.
+ */
+#define DSA_BF16 0 /* dtype: bf16 */
+#define DSA_F32 1  /* dtype: float32 */
+
+/*
+ * Rotary positions.  Pair i (0 <= i < rot_dim / 2) of a token at position p turns by the
+ * angle p f_i, f_i = theta^(-2i / rot_dim):  (a, b) -> m (a cos - b sin, a sin + b cos).
+ *   DSA_ROPE_HALF         a = x[i], b = x[i + rot_dim / 2]
+ *   DSA_ROPE_INTERLEAVED  a = x[2i], b = x[2i + 1]
+ * factor > 1 extends a model's window from orig_len positions: a pair that turns at least
+ * 32 times over orig_len positions keeps f_i, one that turns at most once gets f_i / factor,
+ * and those between are blended linearly over the pair's index (the ends rounded outwards
+ * to whole indices and kept within [0, rot_dim - 1]); m = 0.1 ln(factor) + 1.  factor = 1:
+ * no scaling, m = 1, orig_len unused.
+ *
+ * dsa_rope_init fills a plan on the host (no CUDA call): rot_dim even, 2 .. 256; theta > 1;
+ * factor >= 1, with orig_len >= 1 where factor > 1.  The plan is plain data that a caller
+ * keeps and may copy; it is read before the calls that take it return.
+ */
+#define DSA_ROPE_HALF 0
+#define DSA_ROPE_INTERLEAVED 1
+#define DSA_ROPE_MAX_PAIRS 128
+typedef struct {
+    int rot_dim;
+    int layout;                       /* DSA_ROPE_HALF or DSA_ROPE_INTERLEAVED   */
+    float mscale;                     /* m                                       */
+    double turns[DSA_ROPE_MAX_PAIRS]; /* revolutions per position: f_i / (2 pi)  */
+} dsa_rope_plan;
+
+dsa_status dsa_rope_init(dsa_rope_plan *plan, int rot_dim, int layout, double theta, double factor,
+                         long long orig_len);
+
+/*
+ *   x          [n, heads, dim]  dtype  strides x_token and x_head in elements, dim dense
+ *   positions  [n] i64          |position| <= 2^31; a negative one turns backwards
+ *   out        [n, heads, dim]  dtype  entries [rot_offset, rot_offset + rot_dim) of each
+ *                               head rotated, the others as in x; strides out_token and
+ *                               out_head, no two heads overlapping
+ * out may be x itself (with the same strides: only the rotated entries are written);
+ * otherwise the two must not overlap.  Angles are taken in 64 bits, the rotation in 32,
+ * with one rounding to dtype.  Pointers are aligned to their element only; 16-byte aligned
+ * pointers and strides (and a rot_dim / 2 that is a multiple of 16 bytes in the half
+ * layout) take wide loads.  n = 0 does nothing.
+ */
+dsa_status dsa_rope(const void *x, const long long *positions, long long n, int heads, int dim, int rot_offset,
+                    const dsa_rope_plan *plan, int dtype, long long x_token, long long x_head, void *out,
+                    long long out_token, long long out_head, cudaStream_t stream);
+
+/*
+ * A batch over a paged cache.  Tokens [cu_q[b], cu_q[b + 1]) of the n given are the new ones
+ * of sequence b (a sequence may have none); ctx_len[b] counts its cached tokens, the new ones
+ * among them, so token t sits at position ctx_len[b] - cu_q[b + 1] + t.  Position s of
+ * sequence b is row s % page_size of page table[b][s / page_size].
+ *   cache    [num_pages, page_size, 576] bf16   page_size a multiple of 16
+ *   table    [B, max_pages] i32
+ *   cu_q     [B + 1] i32     non-decreasing; tokens behind cu_q[B] (a padded batch) are
+ *                            neither read nor written
+ *   ctx_len  [B] i32
+ * The lengths and the table are read on the device, so a captured call follows them.  A
+ * position that the table does not hold (behind max_pages, or whose entry is not in
+ * [0, num_pages)) is not there: it is not written, and no query sees it.
+ *
+ * dsa_cache_append writes the new tokens' rows:
+ *   x      [n, 576] bf16, row stride x_stride (a multiple of 8 elements): 512 latent and 64
+ *          rotary entries
+ *   gamma  [512] bf16
+ *   row = [x[0:512] * rsqrt(mean(x[0:512]^2) + eps) * gamma, x[512:576] rotated at the token's
+ *          position], rounded once; plan: rot_dim 64
+ * A page that several sequences share must not receive rows (two of them would write the
+ * same row).  x must not lie in the cache.
+ */
+dsa_status dsa_cache_append(const uint16_t *x, long long x_stride, const uint16_t *gamma, float eps,
+                            const dsa_rope_plan *plan, uint16_t *cache, const int32_t *table, const int32_t *cu_q,
+                            const int32_t *ctx_len, int n, int B, int num_pages, int page_size, int max_pages,
+                            cudaStream_t stream);
+
+/*
+ * Attention of the new tokens over their sequences' cached rows (the new ones among them):
+ *   q    [n, H, 576] bf16        1 <= H <= 128
+ *   out  [n, H, 512] bf16  out:  softmax_s(scale * q . c[s]) weighted sum of c[s][0:512] over
+ *                                the positions s <= the token's own; zero when it sees none
+ *   lse  [n, H] f32 out:         ln sum_s exp(scale * q . c[s]) (-inf when none); may be NULL
+ * bf16 operands (the weights are rounded to bf16 before the product with the values), f32
+ * accumulation and softmax, one rounding of the output.  Rows behind ctx_len[b] may hold
+ * anything, NaN included; the rows of a sequence's cached tokens must be finite.
+ * workspace: dsa_paged_workspace_size(n, B, H) bytes, 256-byte aligned, written by every call
+ * (calls that overlap on the GPU need one each); the size depends on the current device.
+ */
+size_t dsa_paged_workspace_size(int n, int B, int H);
+dsa_status dsa_paged_attn(const uint16_t *q, const uint16_t *cache, const int32_t *table, const int32_t *cu_q,
+                          const int32_t *ctx_len, int n, int B, int H, int num_pages, int page_size, int max_pages,
+                          float scale, uint16_t *out, float *lse, void *workspace, size_t workspace_bytes,
+                          cudaStream_t stream);
+
+/*
+ * Logits to probabilities, for the p and q of dsa_verify (S = 1: a plain sampling step).
+ * Row (b, j) is position j of sequence b; for each entry v, in this order:
+ *   z = logits[b, j, v]
+ *   z = z > 0 ? z / repetition[b] : z * repetition[b]   if v is in the sequence's history or
+ *                                                       among draft[b, 0..j-1]
+ *   z = z - frequency[b] * count - presence[b] * (count > 0)   count: occurrences of v in the
+ *                                   history from prompt_len[b] on and in draft[b, 0..j-1]
+ *   z = z + the sum of the bias_values[b, i] with bias_ids[b, i] == v
+ *   z = -inf                        if bit v % 32 of mask[b, j, v / 32] is 0, or z is NaN
+ *   p = exp((z - max z) / temperature[b]) / sum;  temperature 0 (or not positive): 1 at the
+ *       lowest index of the maximum, 0 elsewhere
+ * A row whose entries are all -inf gets zeros; where the maximum is +inf its entries share
+ * the probability.
+ *   logits       [B, S, V] dtype        p  [B, S, V] f32 out; V < 2^24
+ *   temperature, repetition, frequency, presence  [B] f32  NULL: 1, 1, 0, 0
+ *   history      [B, history_cap] i32   NULL: none; its first history_len[b] entries count
+ *                                       (NULL: all), the first prompt_len[b] (NULL: 0) of
+ *                                       them being the prompt; fewer than 2^30 entries
+ *   draft        [B, S] i32             NULL: none
+ *   bias_ids     [B, nbias] i32, bias_values [B, nbias] f32   NULL: none
+ *   mask         [B, S, ceil(V / 32)] u32   NULL: none
+ * Ids outside [0, V) are skipped (padding).  p must not overlap an input.
+ */
+dsa_status dsa_logits_probs(const void *logits, int dtype, int B, int S, int V, const float *temperature,
+                            const float *repetition, const float *frequency, const float *presence,
+                            const int32_t *history, int history_cap, const int32_t *history_len,
+                            const int32_t *prompt_len, const int32_t *draft, const int32_t *bias_ids,
+                            const float *bias_values, int nbias, const uint32_t *mask, float *p,
+                            cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -34,7 +34,10 @@ EXPORTS = ("dsa_status_string", "dsa_version", "dsa_workspace_size", "dsa_worksp
            "dsa_topk",
            "dsa_sparse_attn", "dsa_group_forward", "dsa_topk_noalloc", "dsa_device_error",
            "dsa_check_device_status", "dsa_last_cuda_error", "dsa_cuda_error_string", "dsa_verify",
-           "dsa_decode_workspace_size", "dsa_decode_step")
+           "dsa_decode_workspace_size", "dsa_decode_step", "dsa_rope_init", "dsa_rope", "dsa_cache_append",
+           "dsa_paged_workspace_size", "dsa_paged_attn", "dsa_logits_probs")
+
+ROPE_LAYOUTS = ("half", "interleaved")  # DSA_ROPE_HALF, DSA_ROPE_INTERLEAVED
 
 
 class GroupIO(ctypes.Structure):
@@ -42,6 +45,12 @@ class GroupIO(ctypes.Structure):
     _fields_ = [("iq", ctypes.c_void_p), ("ik", ctypes.c_void_p), ("w", ctypes.c_void_p),
                 ("q", ctypes.c_void_p * MAX_LAYERS), ("kv", ctypes.c_void_p * MAX_LAYERS), ("idx", ctypes.c_void_p),
                 ("out", ctypes.c_void_p * MAX_LAYERS), ("index_format", ctypes.c_int)]
+
+
+class RopePlan(ctypes.Structure):
+    """dsa_rope_plan: the rotary frequencies, made by dsa_rope_init."""
+    _fields_ = [("rot_dim", ctypes.c_int), ("layout", ctypes.c_int), ("mscale", ctypes.c_float),
+                ("turns", ctypes.c_double * 128)]
 
 
 class DsaError(RuntimeError):
@@ -92,6 +101,16 @@ def lib() -> ctypes.CDLL:
         L.dsa_decode_workspace_size.restype = S
         L.dsa_decode_step.argtypes = [P, I, I, I, I, I, I, F, P, S, P, P]
         L.dsa_decode_step.restype = I
+        D = ctypes.c_double
+        L.dsa_rope_init.argtypes = [P, I, I, D, D, LL]
+        L.dsa_rope.argtypes = [P, P, LL, I, I, I, P, I, LL, LL, P, LL, LL, P]
+        L.dsa_cache_append.argtypes = [P, LL, P, F, P, P, P, P, P, I, I, I, I, I, P]
+        L.dsa_paged_workspace_size.argtypes = [I, I, I]
+        L.dsa_paged_workspace_size.restype = S
+        L.dsa_paged_attn.argtypes = [P, P, P, P, P, I, I, I, I, I, I, F, P, P, P, S, P]
+        L.dsa_logits_probs.argtypes = [P, I, I, I, I, P, P, P, P, P, I, P, P, P, P, P, I, P, P, P]
+        for f in ("dsa_rope_init", "dsa_rope", "dsa_cache_append", "dsa_paged_attn", "dsa_logits_probs"):
+            getattr(L, f).restype = I
         for f in ("dsa_index_score", "dsa_index_score_e4m3", "dsa_sparse_attn_shard", "dsa_shard_candidates",
                   "dsa_merge_candidates", "dsa_merge_partials", "dsa_topk", "dsa_sparse_attn", "dsa_group_forward", "dsa_topk_noalloc",
                   "dsa_verify"):
@@ -421,3 +440,159 @@ def dsa_decode_step(groups, k: int, scale: float, ws=None, stream=None, side=Non
     rc = lib().dsa_decode_step(ctypes.addressof(arr), G, L, B, N, H, int(k), float(scale),
                                _ptr(ws, (torch.uint8,), "workspace"), ws.numel(), _stream(stream), _stream(side))
     _check(rc, "dsa_decode_step")
+
+
+# ---------------------------------------------------------------- around the verify step
+def _device(*tensors):
+    """The CUDA device that all the given tensors (None skipped) lie on."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not isinstance(t, _torch().Tensor):
+            raise TypeError(f"expected a torch.Tensor, got {type(t).__name__}")
+        if not t.is_cuda:
+            raise ValueError("expected CUDA tensors (there is no CPU path)")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}: all must be on one device")
+    return dev
+
+
+def _on(dev, call, stream):
+    """`call(raw stream)` with `dev` current; the default stream is dev's current one."""
+    torch = _torch()
+    if dev.index == torch.cuda.current_device():
+        return call(_stream(stream))
+    with torch.cuda.device(dev):
+        return call(_stream(stream))
+
+
+def dsa_rope_init(rot_dim: int, layout: str = "interleaved", theta: float = 10000.0, factor: float = 1.0,
+                  orig_len: int = 0) -> RopePlan:
+    """The plan of a rotary embedding (see include/dsa.h): `layout` "half" or "interleaved";
+    `factor` > 1 extends a window of `orig_len` positions."""
+    if layout not in ROPE_LAYOUTS:
+        raise ValueError(f"layout {layout!r}, expected one of {ROPE_LAYOUTS}")
+    plan = RopePlan()
+    _check(lib().dsa_rope_init(ctypes.addressof(plan), int(rot_dim), ROPE_LAYOUTS.index(layout), float(theta),
+                               float(factor), int(orig_len)), "dsa_rope_init")
+    return plan
+
+
+def dsa_rope(x, positions, plan: RopePlan, rot_offset: int = 0, out=None, stream=None):
+    """x [n, heads, dim] bf16 or f32 (last dimension dense, the others strided as they are),
+    positions [n] int64 -> out: entries [rot_offset, rot_offset + plan.rot_dim) of each head
+    rotated, the others copied.  `out` may be x (in place) or a strided tensor apart from it."""
+    torch = _torch()
+    n, heads, dim = x.shape
+    if out is None:
+        out = torch.empty((n, heads, dim), dtype=x.dtype, device=x.device)
+    dev = _device(x, positions, out)
+    if x.dtype not in (torch.bfloat16, torch.float32) or out.dtype != x.dtype:
+        raise TypeError(f"x and out must both be bf16 or both float32, got {x.dtype} and {out.dtype}")
+    if out.shape != x.shape or (dim > 1 and (x.stride(2) != 1 or out.stride(2) != 1)):
+        raise ValueError("out must have x's shape, and both a dense last dimension")
+    args = (x.data_ptr(), _ptr(positions, (torch.int64,), "positions", (n,)), n, heads, dim, int(rot_offset),
+            ctypes.addressof(plan), int(x.dtype == torch.float32), x.stride(0), x.stride(1), out.data_ptr(), out.stride(0),
+            out.stride(1))
+    if n and heads:
+        _check(_on(dev, lambda s: lib().dsa_rope(*args, s), stream), "dsa_rope")
+    return out
+
+
+def _paged(n, cache, table, cu_q, ctx_len):
+    """Checked pointers and sizes of a paged batch, as the C calls take them."""
+    torch = _torch()
+    if cache.dim() != 3 or table.dim() != 2:
+        raise ValueError("cache must be [pages, page_size, 576] and table [B, max_pages]")
+    P, page, _ = cache.shape
+    B, most = table.shape
+    i32 = (torch.int32,)
+    return (_ptr(cache, _bf16_types(), "cache", (P, page, DQK)), _ptr(table, i32, "table"),
+            _ptr(cu_q, i32, "cu_q", (B + 1,)), _ptr(ctx_len, i32, "ctx_len", (B,))), (n, B), (P, page, most)
+
+
+def dsa_cache_append(x, gamma, eps: float, plan: RopePlan, cache, table, cu_q, ctx_len, stream=None):
+    """Normalises, rotates and writes the new tokens' rows x [n, 576] bf16 (rows may be
+    strided) to the pages of their sequences; gamma [512] bf16, cache [pages, page_size, 576]
+    bf16, table [B, max_pages], cu_q [B+1] and ctx_len [B] int32.  Returns cache."""
+    dev = _device(x, gamma, cache, table, cu_q, ctx_len)
+    if x.dtype not in _bf16_types() or x.dim() != 2 or x.shape[1] != DQK or x.stride(1) != 1:
+        raise ValueError(f"x must be [n, {DQK}] bf16 with dense rows")
+    n = x.shape[0]
+    ptrs, sizes, pages = _paged(n, cache, table, cu_q, ctx_len)
+    args = (x.data_ptr(), x.stride(0) if n > 1 else DQK, _ptr(gamma, _bf16_types(), "gamma", (DV,)), float(eps),
+            ctypes.addressof(plan), *ptrs, *sizes, *pages)
+    if n:
+        _check(_on(dev, lambda s: lib().dsa_cache_append(*args, s), stream), "dsa_cache_append")
+    return cache
+
+
+def paged_workspace(n: int, B: int, H: int, device=None):
+    """A workspace tensor for dsa_paged_attn with up to n tokens, B sequences and H heads."""
+    torch = _torch()
+    dev = torch.device(device or "cuda")
+    with torch.cuda.device(dev):
+        size = int(lib().dsa_paged_workspace_size(n, B, H))
+    if size == 0:
+        raise ValueError("invalid sizes for dsa_paged_workspace_size")
+    return torch.empty(size, dtype=torch.uint8, device=dev)
+
+
+def dsa_paged_attn(q, cache, table, cu_q, ctx_len, scale: float, out=None, lse=None, ws=None, stream=None):
+    """Attention of the new tokens q [n, H, 576] bf16 over their sequences' rows in a paged
+    cache (see dsa_cache_append) -> (out [n, H, 512] bf16, lse [n, H] f32)."""
+    torch = _torch()
+    n, H, _ = q.shape
+    if out is None:
+        out = torch.empty((n, H, DV), dtype=torch.bfloat16, device=q.device)
+    if lse is None:
+        lse = torch.empty((n, H), dtype=torch.float32, device=q.device)
+    if ws is None:
+        ws = paged_workspace(n, table.shape[0], H, q.device)
+    dev = _device(q, cache, table, cu_q, ctx_len, out, lse, ws)
+    ptrs, sizes, pages = _paged(n, cache, table, cu_q, ctx_len)
+    args = (_ptr(q, _bf16_types(), "q", (n, H, DQK)), *ptrs, *sizes, H, *pages, float(scale),
+            _ptr(out, _bf16_types(), "out", (n, H, DV)), _ptr(lse, (torch.float32,), "lse", (n, H)),
+            _ptr(ws, (torch.uint8,), "workspace"), ws.numel())
+    if n:
+        _check(_on(dev, lambda s: lib().dsa_paged_attn(*args, s), stream), "dsa_paged_attn")
+    return out, lse
+
+
+def dsa_logits_probs(logits, temperature=None, history=None, history_len=None, prompt_len=None, draft=None,
+                     repetition=None, frequency=None, presence=None, bias_ids=None, bias_values=None, mask=None, out=None,
+                     stream=None):
+    """logits [B, S, V] f32 or bf16 -> p [B, S, V] f32 for dsa_verify (see include/dsa.h):
+    penalties over history [B, cap] int32 (its first history_len[b], of which prompt_len[b]
+    are the prompt) and the drafts before a row (draft [B, S] int32), biases (bias_ids and
+    bias_values [B, nb]), an allow mask (mask [B, S, ceil(V/32)] int32 bits), and the softmax
+    at temperature [B] (0: one-hot at the maximum)."""
+    torch = _torch()
+    B, S, V = logits.shape
+    if out is None:
+        out = torch.empty((B, S, V), dtype=torch.float32, device=logits.device)
+    dev = _device(logits, temperature, history, history_len, prompt_len, draft, repetition, frequency, presence, bias_ids,
+                  bias_values, mask, out)
+    f32, i32 = (torch.float32,), (torch.int32,)
+    cap = nb = 0
+    if history is not None:
+        cap = history.shape[1]
+    elif history_len is not None or prompt_len is not None:
+        raise ValueError("history_len and prompt_len need a history")
+    if (bias_ids is None) != (bias_values is None):
+        raise ValueError("bias_ids and bias_values go together")
+    if bias_ids is not None:
+        nb = bias_ids.shape[1]
+    args = (_ptr(logits, (torch.float32, torch.bfloat16), "logits"), int(logits.dtype == torch.float32), B, S, V,
+            _ptr(temperature, f32, "temperature", (B,)), _ptr(repetition, f32, "repetition", (B,)),
+            _ptr(frequency, f32, "frequency", (B,)), _ptr(presence, f32, "presence", (B,)),
+            _ptr(history, i32, "history", (B, cap)), cap, _ptr(history_len, i32, "history_len", (B,)),
+            _ptr(prompt_len, i32, "prompt_len", (B,)), _ptr(draft, i32, "draft", (B, S)),
+            _ptr(bias_ids, i32, "bias_ids", (B, nb)), _ptr(bias_values, f32, "bias_values", (B, nb)), nb,
+            _ptr(mask, i32, "mask", (B, S, (V + 31) // 32)), _ptr(out, f32, "out", (B, S, V)))
+    if B and S:
+        _check(_on(dev, lambda s: lib().dsa_logits_probs(*args, s), stream), "dsa_logits_probs")
+    return out

@@ -5,6 +5,7 @@
 // by all 4) and "GLM-5.2 MTP IndexShare inference", Indexer Share in the MTP layer (draft
 // steps 2.. reuse the step-1 index list, so draft-token rows are never attended; the MTP
 // layer reads the target cache -- KV Share).
+#include <cmath>
 #include <cstdio>
 #include <vector>
 
@@ -245,6 +246,21 @@ cudaError_t read_error_words(cudaStream_t stream, bool clear, ErrorWords* w) {
   return cudaSuccess;
 }
 
+bool rope_plan_ok(const dsa_rope_plan* p) {
+  return p && p->rot_dim >= 2 && p->rot_dim <= 2 * DSA_ROPE_MAX_PAIRS && p->rot_dim % 2 == 0 &&
+         (p->layout == DSA_ROPE_HALF || p->layout == DSA_ROPE_INTERLEAVED);
+}
+
+// The checks that the append and the attention over a paged cache share.
+dsa_status check_paged(const void* cache, const int32_t* table, const int32_t* cu_q, const int32_t* ctx_len, int n, int B,
+                       int num_pages, int page_size, int max_pages) {
+  if (!cache || !table || !cu_q || !ctx_len || n < 0 || B <= 0 || num_pages <= 0 || page_size <= 0 || max_pages <= 0)
+    return DSA_ERR_INVALID_ARG;
+  if (!aligned(cache, 16) || !aligned(table, 4) || !aligned(cu_q, 4) || !aligned(ctx_len, 4)) return DSA_ERR_INVALID_ARG;
+  if (page_size % 16 != 0 || (long long)num_pages * page_size > 0x7FFFFFFFLL) return DSA_ERR_UNSUPPORTED;
+  return DSA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -266,7 +282,7 @@ const char* dsa_status_string(int status) {
   }
 }
 
-int dsa_version(void) { return 10000; }
+int dsa_version(void) { return 10100; }
 
 dsa_status dsa_device_error(int* code, int clear) {
   if (!code) return DSA_ERR_INVALID_ARG;
@@ -496,6 +512,132 @@ dsa_status dsa_verify(const float* p, const float* q, const int32_t* draft, cons
       !aligned(u2, 4) || !aligned(accept, 4) || !aligned(token, 4) || !aligned(accepted_len, 4))
     return DSA_ERR_INVALID_ARG;
   return cuda_status(launch_verify(p, q, draft, u, u2, B, S, V, alpha, accept, token, accepted_len, stream));
+}
+
+dsa_status dsa_rope_init(dsa_rope_plan* plan, int rot_dim, int layout, double theta, double factor, long long orig_len) {
+  if (!plan || rot_dim < 2 || rot_dim % 2 != 0 || !(theta > 1.0) || !(factor >= 1.0) || std::isinf(theta) ||
+      std::isinf(factor) || (factor > 1.0 && orig_len < 1) || (layout != DSA_ROPE_HALF && layout != DSA_ROPE_INTERLEAVED))
+    return DSA_ERR_INVALID_ARG;
+  if (rot_dim > 2 * DSA_ROPE_MAX_PAIRS) return DSA_ERR_UNSUPPORTED;
+  const double two_pi = 6.283185307179586476925;
+  double lo = 0, hi = 0;
+  if (factor > 1.0) {
+    // index of the pair that turns so many times over orig_len positions
+    auto pair = [&](double times) { return rot_dim * std::log(orig_len / (times * two_pi)) / (2.0 * std::log(theta)); };
+    lo = std::fmax(std::floor(pair(32.0)), 0.0);
+    hi = std::fmin(std::ceil(pair(1.0)), rot_dim - 1.0);
+  }
+  plan->rot_dim = rot_dim;
+  plan->layout = layout;
+  plan->mscale = factor > 1.0 ? (float)(0.1 * std::log(factor) + 1.0) : 1.f;
+  for (int i = 0; i < DSA_ROPE_MAX_PAIRS; ++i) {
+    double f = i < rot_dim / 2 ? std::pow(theta, -2.0 * i / rot_dim) : 0.0;
+    if (factor > 1.0) {
+      const double r = std::fmin(std::fmax((i - lo) / std::fmax(hi - lo, 0.001), 0.0), 1.0);
+      f = f * (1.0 - r) + f / factor * r;
+    }
+    plan->turns[i] = f / two_pi;
+  }
+  return DSA_OK;
+}
+
+dsa_status dsa_rope(const void* x, const long long* positions, long long n, int heads, int dim, int rot_offset,
+                    const dsa_rope_plan* plan, int dtype, long long x_token, long long x_head, void* out,
+                    long long out_token, long long out_head, cudaStream_t stream) {
+  if (!x || !positions || !out || !rope_plan_ok(plan) || n < 0 || heads <= 0 || dim <= 0 || rot_offset < 0 ||
+      (long long)rot_offset + plan->rot_dim > dim)
+    return DSA_ERR_INVALID_ARG;
+  if (dtype != DSA_BF16 && dtype != DSA_F32) return DSA_ERR_UNSUPPORTED;
+  const size_t esz = dtype == DSA_F32 ? 4 : 2;
+  if (!aligned(x, esz) || !aligned(out, esz) || !aligned(positions, 8)) return DSA_ERR_INVALID_ARG;
+  if (x_token < 0 || x_head < 0 || out_token < 0 || out_head < 0) return DSA_ERR_INVALID_ARG;
+  if (x == out && (x_token != out_token || x_head != out_head)) return DSA_ERR_INVALID_ARG;
+  // heads of the output must not overlap, tokens outermost or heads outermost
+  const long long reach = 1LL << 40;
+  if (n > reach / heads / dim || x_token > reach || x_head > reach || out_token > reach || out_head > reach)
+    return DSA_ERR_UNSUPPORTED;
+  const bool tokens_out = (heads == 1 || out_head >= dim) && (n <= 1 || out_token >= (heads - 1) * out_head + dim);
+  const bool heads_out = (n <= 1 || out_token >= dim) && (heads == 1 || out_head >= (n - 1) * out_token + dim);
+  if (!tokens_out && !heads_out) return DSA_ERR_INVALID_ARG;
+  if (n == 0) return DSA_OK;
+  return cuda_status(
+      launch_rope(x, positions, n, heads, dim, rot_offset, *plan, dtype, x_token, x_head, out, out_token, out_head, stream));
+}
+
+dsa_status dsa_cache_append(const uint16_t* x, long long x_stride, const uint16_t* gamma, float eps,
+                            const dsa_rope_plan* plan, uint16_t* cache, const int32_t* table, const int32_t* cu_q,
+                            const int32_t* ctx_len, int n, int B, int num_pages, int page_size, int max_pages,
+                            cudaStream_t stream) {
+  if (!x || !gamma || !rope_plan_ok(plan) || !(eps >= 0.f)) return DSA_ERR_INVALID_ARG;
+  const dsa_status st = check_paged(cache, table, cu_q, ctx_len, n, B, num_pages, page_size, max_pages);
+  if (st != DSA_OK) return st;
+  if (!aligned(x, 16) || !aligned(gamma, 16) || x_stride < (n > 1 ? kDqk : 0) || x_stride % 8 != 0)
+    return DSA_ERR_INVALID_ARG;
+  if (plan->rot_dim != kDqk - kDv) return DSA_ERR_UNSUPPORTED;
+  if (n == 0) return DSA_OK;
+  const PagedBatch pb{table, cu_q, ctx_len, n, B, max_pages, num_pages, page_size};
+  return cuda_status(launch_cache_append(x, x_stride, gamma, eps, *plan, pb, cache, stream));
+}
+
+size_t dsa_paged_workspace_size(int n, int B, int H) {
+  if (n < 0 || B <= 0 || H <= 0 || H > 128 || (long long)n * H > 0x7FFFFFFFLL) return 0;
+  return paged_attn_workspace_bytes(n, B, H);
+}
+
+dsa_status dsa_paged_attn(const uint16_t* q, const uint16_t* cache, const int32_t* table, const int32_t* cu_q,
+                          const int32_t* ctx_len, int n, int B, int H, int num_pages, int page_size, int max_pages,
+                          float scale, uint16_t* out, float* lse, void* workspace, size_t workspace_bytes,
+                          cudaStream_t stream) {
+  if (!q || !out || H <= 0 || !std::isfinite(scale)) return DSA_ERR_INVALID_ARG;
+  const dsa_status st = check_paged(cache, table, cu_q, ctx_len, n, B, num_pages, page_size, max_pages);
+  if (st != DSA_OK) return st;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4)) return DSA_ERR_INVALID_ARG;
+  if (H > 128 || (long long)n * H > 0x7FFFFFFFLL) return DSA_ERR_UNSUPPORTED;
+  if (n == 0) return DSA_OK;
+  const size_t need = paged_attn_workspace_bytes(n, B, H);
+  if (need == 0) return cuda_status(cudaErrorInvalidDevice);
+  if (!workspace || workspace_bytes < need || !aligned(workspace, 256)) return DSA_ERR_WORKSPACE;
+  const PagedBatch pb{table, cu_q, ctx_len, n, B, max_pages, num_pages, page_size};
+  return cuda_status(launch_paged_attn(q, cache, pb, H, scale, out, lse, workspace, stream));
+}
+
+dsa_status dsa_logits_probs(const void* logits, int dtype, int B, int S, int V, const float* temperature,
+                            const float* repetition, const float* frequency, const float* presence,
+                            const int32_t* history, int history_cap, const int32_t* history_len,
+                            const int32_t* prompt_len, const int32_t* draft, const int32_t* bias_ids,
+                            const float* bias_values, int nbias, const uint32_t* mask, float* p, cudaStream_t stream) {
+  if (!logits || !p || B < 0 || S < 0 || V <= 0 || V >= (1 << 24) || history_cap < 0 || nbias < 0 ||
+      (long long)B * S > 0x7FFFFFFFLL || (nbias > 0 && (!bias_ids || !bias_values)))
+    return DSA_ERR_INVALID_ARG;
+  if (dtype != DSA_BF16 && dtype != DSA_F32) return DSA_ERR_UNSUPPORTED;
+  if (history_cap >= (1 << 30)) return DSA_ERR_UNSUPPORTED;
+  if (!aligned(logits, dtype == DSA_F32 ? 4 : 2)) return DSA_ERR_INVALID_ARG;
+  const void* words[] = {p,       temperature, repetition, frequency, presence,    history,
+                         history_len, prompt_len,  draft,      bias_ids,  bias_values, mask};
+  for (const void* w : words)
+    if (!aligned(w, 4)) return DSA_ERR_INVALID_ARG;
+  if ((long long)B * S == 0) return DSA_OK;
+  ProbsArgs a{};
+  a.logits = logits;
+  a.p = p;
+  a.temperature = temperature;
+  a.repetition = repetition;
+  a.frequency = frequency;
+  a.presence = presence;
+  a.history = history_cap > 0 ? history : nullptr;
+  a.history_len = history_len;
+  a.prompt_len = prompt_len;
+  a.draft = draft;
+  a.bias_ids = bias_ids;
+  a.bias_values = bias_values;
+  a.mask = mask;
+  a.dtype = dtype;
+  a.B = B;
+  a.S = S;
+  a.V = V;
+  a.history_cap = history_cap;
+  a.nbias = nbias;
+  return cuda_status(launch_probs(a, stream));
 }
 
 }  // extern "C"

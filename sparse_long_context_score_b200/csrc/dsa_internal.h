@@ -8,6 +8,7 @@
 #include <atomic>
 
 #include "dsa.h"
+#include "paged.cuh"
 
 namespace dsa {
 
@@ -150,5 +151,31 @@ cudaError_t launch_merge_candidates(const float* cand_score, const int32_t* cand
                                     int k, int32_t* idx, cudaStream_t stream);
 cudaError_t launch_merge_partials(const float* outs, const float* lses, int W, long long R, float* out,
                                   cudaStream_t stream);
+
+// rotary positions and the paged cache's rows (rope.cu)
+cudaError_t launch_rope(const void* x, const long long* positions, long long n, int heads, int dim, int rot_offset,
+                        const dsa_rope_plan& plan, int dtype, long long x_token, long long x_head, void* out,
+                        long long out_token, long long out_head, cudaStream_t stream);
+cudaError_t launch_cache_append(const uint16_t* x, long long x_stride, const uint16_t* gamma, float eps,
+                                const dsa_rope_plan& plan, const PagedBatch& pb, uint16_t* cache, cudaStream_t stream);
+
+// chunk attention over a paged cache (paged_attn.cu); 0 bytes when the device cannot be
+// queried
+size_t paged_attn_workspace_bytes(long long n, int B, int H);
+cudaError_t launch_paged_attn(const uint16_t* q, const uint16_t* cache, const PagedBatch& pb, int H, float scale,
+                              uint16_t* out, float* lse, void* workspace, cudaStream_t stream);
+
+// logits to probabilities (probs.cu); null pointers: no such step
+struct ProbsArgs {
+  const void* logits;  // [B][S][V], dtype DSA_BF16 or DSA_F32
+  float* p;            // [B][S][V]
+  const float *temperature, *repetition, *frequency, *presence;  // [B]
+  const int32_t *history, *history_len, *prompt_len, *draft;     // [B][history_cap], [B], [B], [B][S]
+  const int32_t* bias_ids;   // [B][nbias]
+  const float* bias_values;  // [B][nbias]
+  const uint32_t* mask;      // [B][S][ceil(V / 32)]
+  int dtype, B, S, V, history_cap, nbias;
+};
+cudaError_t launch_probs(const ProbsArgs& a, cudaStream_t stream);
 
 }  // namespace dsa

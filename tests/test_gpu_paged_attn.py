@@ -1,0 +1,203 @@
+"""dsa_paged_attn against its definition in 64 bits."""
+import math
+
+import pytest
+import torch
+
+from verify_step import DQK, DV, Batch, attention, attention_bounds
+
+pytestmark = pytest.mark.gpu
+SCALE = 1 / 24
+
+
+@pytest.fixture(scope="module")
+def dsa():
+    import sparse_long_context_score_b200 as m
+    from sparse_long_context_score_b200 import build
+    build.build()
+    m.lib()
+    return m
+
+
+def _queries(n, H, seed=7, std=1.0):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return (torch.randn((n, H, DQK), generator=g, device="cuda") * std).to(torch.bfloat16)
+
+
+def _check(got, batch, q, scale=SCALE, table=None):
+    out, lse, size, reach = attention(batch, q, scale, table)
+    most = max(batch.ctx + [1])
+    b_out, b_lse = attention_bounds(out, lse, size, reach, most)
+    none = lse == -math.inf
+    o, l = got[0][:batch.n].double(), got[1][:batch.n].double()
+    assert bool((l[none] == -math.inf).all()) and bool((o[none] == 0).all())
+    assert bool(o.isfinite().all())
+    err = (o - out).abs()
+    assert bool((err <= b_out).all()), f"out: {float((err - b_out).max())} over the bound"
+    err = (l[~none] - lse[~none]).abs()
+    assert bool((err <= b_lse[~none]).all()), f"lse: {float((err - b_lse[~none]).max())} over the bound"
+
+
+CASES = [
+    # new tokens, cached tokens, heads, page
+    ([1], [1], 16, 16),
+    ([1] * 6, [1, 63, 64, 65, 127, 128], 64, 64),
+    ([1] * 5, [129, 255, 256, 257, 1000], 32, 16),
+    ([3, 0, 5, 1], [3, 9, 700, 64], 48, 48),
+    ([2, 1], [130, 77], 1, 16),
+    ([7, 4], [300, 4], 3, 80),
+    ([9], [400], 5, 32),
+    ([3, 2], [140, 513], 128, 256),
+    ([200], [200], 16, 64),
+    ([130, 1, 66], [130, 900, 1000], 64, 128),
+    ([1, 1, 1], [5000, 12345, 20000], 64, 64),
+    ([8, 8], [6001, 300], 64, 16),
+    ([0, 0, 1, 0], [0, 4, 200, 0], 16, 16),
+    ([1] * 300, [1 + (37 * i) % 500 for i in range(300)], 16, 16),
+    ([1], [70000], 16, 128),
+]
+
+
+@pytest.mark.parametrize("new,ctx,heads,page", CASES)
+def test_matches_its_definition(dsa, new, ctx, heads, page):
+    batch = Batch(new, ctx, page, seed=heads + page).fill()
+    q = _queries(batch.n, heads)
+    _check(dsa.dsa_paged_attn(q, batch.cache, batch.table, batch.cu_q, batch.ctx_len, SCALE), batch, q)
+    assert dsa.dsa_check_device_status() == 0
+
+
+@pytest.mark.parametrize("std,order", [(1.0, 1), (4.0, 1), (4.0, -1), (0.0, 1)])
+def test_sharp_flat_and_growing_logits(dsa, std, order):
+    """Logits of hundreds, whose running maximum grows (or falls) along the row; all equal."""
+    batch = Batch([1, 6], [1500, 900], 64, seed=3).fill(std=std)
+    flat = batch.cache.view(-1, DQK)
+    for b in range(2):
+        r = batch.rows(b).cuda()
+        ramp = torch.linspace(0.05, 1.0, len(r), device="cuda")
+        flat[r] = (flat[r].float() * (ramp if order > 0 else ramp.flip(0))[:, None]).to(torch.bfloat16)
+    q = _queries(batch.n, 64, std=4.0)
+    _check(dsa.dsa_paged_attn(q, batch.cache, batch.table, batch.cu_q, batch.ctx_len, SCALE), batch, q)
+    _check(dsa.dsa_paged_attn(q, batch.cache, batch.table, batch.cu_q, batch.ctx_len, -0.5 * SCALE), batch, q, -0.5 * SCALE)
+    _check(dsa.dsa_paged_attn(q, batch.cache, batch.table, batch.cu_q, batch.ctx_len, 0.0), batch, q, 0.0)
+
+
+@pytest.mark.parametrize("heads", [16, 64])
+def test_tokens_that_see_nothing_and_rows_that_are_not_there(dsa, heads):
+    # sequence 0 has more new tokens than cached ones: its first three see nothing
+    new, ctx, page = [5, 2, 4, 1, 1], [2, 300, 500, 40, 90], 16
+    batch = Batch(new, ctx, page, seed=4).fill()
+    batch.table[1, 3], batch.table[1, 18] = -1, batch.P          # bad entries inside and at the end
+    batch.table[2, :20] = -(1 << 31)
+    batch.table[3, :] = 1 << 30                                  # a sequence with no page at all
+    batch.table = batch.table[:, :30].contiguous()               # sequence 2 loses its last pages
+    q = _queries(batch.n, heads)
+    _check(dsa.dsa_paged_attn(q, batch.cache, batch.table, batch.cu_q, batch.ctx_len, SCALE), batch, q)
+
+
+def test_a_padded_batch_leaves_the_rows_behind_alone(dsa):
+    batch = Batch([3, 1], [90, 200], 32).fill()
+    q = _queries(batch.n + 5, 32)
+    q[batch.n:] = math.nan
+    out = torch.full((batch.n + 5, 32, DV), 3.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((batch.n + 5, 32), 5.0, device="cuda")
+    got = dsa.dsa_paged_attn(q, batch.cache, batch.table, batch.cu_q, batch.ctx_len, SCALE, out=out, lse=lse)
+    assert got[0] is out and got[1] is lse
+    _check(got, batch, q[:batch.n])
+    assert bool((out[batch.n:] == 3).all()) and bool((lse[batch.n:] == 5).all())
+
+
+def test_pages_shared_by_sequences_and_extra_table_columns(dsa):
+    batch = Batch([2, 2], [256, 256], 64, extra_columns=9).fill()
+    batch.table[1, :3] = batch.table[0, :3]
+    q = _queries(batch.n, 16)
+    _check(dsa.dsa_paged_attn(q, batch.cache, batch.table, batch.cu_q, batch.ctx_len, SCALE), batch, q)
+
+
+def test_repeats_bit_for_bit_and_ignores_the_workspace(dsa):
+    batch = Batch([4, 1, 9], [3000, 9000, 700], 64).fill()
+    q = _queries(batch.n, 64)
+    first = dsa.dsa_paged_attn(q, batch.cache, batch.table, batch.cu_q, batch.ctx_len, SCALE)
+    ws = dsa.paged_workspace(batch.n, 3, 64)
+    for fill in (0, 255, 127):
+        ws.fill_(fill)
+        again = dsa.dsa_paged_attn(q, batch.cache, batch.table, batch.cu_q, batch.ctx_len, SCALE, ws=ws)
+        assert torch.equal(again[0], first[0]) and torch.equal(again[1], first[1])
+
+
+def test_a_captured_call_follows_the_lengths_and_the_table(dsa):
+    """One graph, replayed while the chats grow, sequences leave and pages move."""
+    steps = [([1, 1, 1], [100, 2000, 17]), ([1, 1, 1], [101, 2001, 18]), ([1, 0, 1], [5000, 0, 64]), ([0, 1, 0], [0, 1, 0])]
+    n, columns, page, pool = 3, 80, 64, 128
+    q = _queries(n, 32)
+    cache = torch.zeros((pool, page, DQK), dtype=torch.bfloat16, device="cuda")
+    table = torch.zeros((3, columns), dtype=torch.int32, device="cuda")
+    cu_q, ctx_len = torch.zeros(4, dtype=torch.int32, device="cuda"), torch.zeros(3, dtype=torch.int32, device="cuda")
+    out, lse = torch.zeros((n, 32, DV), dtype=torch.bfloat16, device="cuda"), torch.zeros((n, 32), device="cuda")
+    ws = dsa.paged_workspace(n, 3, 32)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        dsa.dsa_paged_attn(q, cache, table, cu_q, ctx_len, SCALE, out=out, lse=lse, ws=ws)
+    stream.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dsa.dsa_paged_attn(q, cache, table, cu_q, ctx_len, SCALE, out=out, lse=lse, ws=ws)
+    for i, (new, ctx) in enumerate(steps):
+        batch = Batch(new, ctx, page, seed=i).fill(seed=i)
+        cache[:batch.P] = batch.cache
+        table.fill_(-1)
+        table[:, :batch.table.shape[1]] = batch.table
+        cu_q.copy_(batch.cu_q)
+        ctx_len.copy_(batch.ctx_len)
+        graph.replay()
+        torch.cuda.synchronize()
+        _check((out, lse), batch, q[:batch.n])
+
+
+def test_another_stream(dsa):
+    batch = Batch([2], [4000], 64).fill()
+    q = _queries(2, 64)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    out, lse = torch.empty((2, 64, DV), dtype=torch.bfloat16, device="cuda"), torch.empty((2, 64), device="cuda")
+    ws = dsa.paged_workspace(2, 1, 64)
+    dsa.dsa_paged_attn(q, batch.cache, batch.table, batch.cu_q, batch.ctx_len, SCALE, out=out, lse=lse, ws=ws, stream=side)
+    side.synchronize()
+    _check((out, lse), batch, q)
+
+
+def test_offsets_past_32_bits(dsa):
+    """A pool of 5 GB: the last pages start behind 2^32 bytes."""
+    batch = Batch([1], [400], 64)
+    pages = (5 << 30) // (64 * DQK * 2)
+    cache = torch.zeros((pages, 64, DQK), dtype=torch.bfloat16, device="cuda")
+    batch.table = torch.tensor([[pages - 1, 3, pages - 5, pages - 2, 0, pages - 3, pages - 4]], dtype=torch.int32, device="cuda")
+    batch.cache, batch.P = cache, pages
+    batch.fill()
+    q = _queries(1, 64)
+    _check(dsa.dsa_paged_attn(q, cache, batch.table, batch.cu_q, batch.ctx_len, SCALE), batch, q)
+
+
+def test_binding_refusals(dsa):
+    batch = Batch([1], [20], 16).fill()
+    q = _queries(1, 16)
+    args = (batch.cache, batch.table, batch.cu_q, batch.ctx_len, SCALE)
+    with pytest.raises(ValueError):
+        dsa.dsa_paged_attn(q[..., :570], *args)
+    with pytest.raises(TypeError):
+        dsa.dsa_paged_attn(q.float(), *args)
+    with pytest.raises(TypeError):
+        dsa.dsa_paged_attn(q, batch.cache, batch.table.long(), batch.cu_q, batch.ctx_len, SCALE)
+    with pytest.raises(ValueError):
+        dsa.dsa_paged_attn(q, batch.cache, batch.table, batch.cu_q[:1], batch.ctx_len, SCALE)
+    with pytest.raises(ValueError):
+        dsa.dsa_paged_attn(q.cpu(), *args, ws=torch.empty(1, dtype=torch.uint8))
+    with pytest.raises(dsa.DsaError) as err:
+        dsa.dsa_paged_attn(q, *args, ws=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    assert err.value.status == -3
+    with pytest.raises(dsa.DsaError) as err:
+        dsa.dsa_paged_attn(q, batch.cache.view(-1, 8, DQK), *args[1:])
+    assert err.value.status == -2
+    none = dsa.dsa_paged_attn(q[:0], *args)
+    assert none[0].shape == (0, 16, DV)

@@ -1,0 +1,246 @@
+"""dsa_logits_probs against its definition in 64 bits, and the whole verify step."""
+import math
+
+import pytest
+import torch
+
+from verify_step import DQK, DV, Batch, attention, attention_bounds, probabilities, rope, frequencies
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def dsa():
+    import sparse_long_context_score_b200 as m
+    from sparse_long_context_score_b200 import build
+    build.build()
+    m.lib()
+    return m
+
+
+def _gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def _inputs(B, S, V, seed=0, dtype=torch.float32, hist=0, bias=0, mask=False, greedy=()):
+    g = _gen(seed)
+    u = lambda lo, hi: lo + (hi - lo) * torch.rand(B, generator=g, device="cuda")  # noqa: E731
+    a = dict(logits=(torch.randn((B, S, V), generator=g, device="cuda") * 3).to(dtype), temperature=u(0.4, 1.5))
+    for b in greedy:
+        a["temperature"][b] = 0.0
+    if hist:
+        a["history"] = torch.randint(-2, min(V + 2, 300), (B, hist), generator=g, device="cuda", dtype=torch.int32)
+        a["history_len"] = torch.randint(0, hist + 5, (B,), generator=g, device="cuda", dtype=torch.int32)
+        a["prompt_len"] = torch.randint(0, hist, (B,), generator=g, device="cuda", dtype=torch.int32)
+        a["draft"] = torch.randint(-1, min(V + 1, 300), (B, S), generator=g, device="cuda", dtype=torch.int32)
+        a["repetition"], a["frequency"], a["presence"] = u(0.8, 1.4), u(-0.3, 0.6), u(-0.3, 0.6)
+    if bias:
+        a["bias_ids"] = torch.randint(-1, min(V + 1, 2 * bias), (B, bias), generator=g, device="cuda", dtype=torch.int32)
+        a["bias_values"] = torch.randn((B, bias), generator=g, device="cuda") * 3
+    if mask:
+        a["mask"] = torch.randint(-(1 << 31), 1 << 31, (B, S, (V + 31) // 32), generator=g, device="cuda").to(torch.int32)
+    return a
+
+
+def _check(dsa, a):
+    got = dsa.dsa_logits_probs(**a).cpu().double()
+    p, size = probabilities(**a)
+    B, S, V = p.shape
+    T = torch.ones(B) if a.get("temperature") is None else a["temperature"].cpu()
+    T = torch.where(T > 0, T, 1.0).double()[:, None, None].expand(B, S, 1)
+    nb = 0 if a.get("bias_ids") is None else a["bias_ids"].shape[1]
+    # a logit takes at most 8 roundings and its biases' on the way to the exponent, each half a
+    # step of the largest value passed; the exponential is good to 2^-22, the sum of V terms to
+    # 1024 half steps (its additions are at most that deep)
+    dz = (8 + nb) * 2.0 ** -24 * size[..., None] / T
+    exponent = -torch.where(p > 0, p, 1.0).log()
+    bound = p * (2 * dz + 4 * 2.0 ** -24 * exponent.abs() + 2.0 ** -21 + 1024 * 2.0 ** -24) + 1e-37
+    err = (got - p).abs()
+    assert bool((err <= bound).all()), f"{float((err - bound).max())} over the bound"
+    greedy = (a["temperature"].cpu() <= 0) if a.get("temperature") is not None else torch.zeros(B, dtype=torch.bool)
+    assert torch.equal(got[greedy], p[greedy])
+    return got
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("B,S,V,kw", [
+    (1, 1, 1, {}), (1, 1, 2, dict(mask=True)), (2, 3, 31, dict(hist=9, bias=3, mask=True)), (3, 1, 33, dict(greedy=(1,))),
+    (2, 2, 1000, dict(hist=200, bias=20, mask=True, greedy=(0,))), (1, 4, 4097, dict(hist=50)),
+    (5, 1, 20480, dict(bias=5)), (2, 1, 32003, dict(mask=True)), (1, 7, 50257, dict(hist=3000, bias=100, mask=True)),
+    (2, 2, 151552, dict(hist=1000, bias=8, mask=True, greedy=(1,))), (1, 2, 163841, dict(hist=100)),
+    (1, 1, 262144, dict(mask=True, hist=10)), (1, 1, 327681, {}), (1, 1, 700001, dict(hist=64, bias=4, mask=True))])
+def test_matches_its_definition(dsa, dtype, B, S, V, kw):
+    _check(dsa, _inputs(B, S, V, seed=V, dtype=dtype, **kw))
+
+
+def test_each_step_alone(dsa):
+    full = _inputs(3, 4, 5003, seed=1, hist=400, bias=30, mask=True, greedy=(2,))
+    for keep in [(), ("history",), ("draft",), ("history", "repetition"), ("history", "history_len", "frequency"),
+                 ("history", "prompt_len", "presence"), ("draft", "repetition", "presence"), ("draft", "frequency"),
+                 ("bias_ids", "bias_values"), ("mask",), ("temperature",), ("repetition", "frequency", "presence")]:
+        _check(dsa, {"logits": full["logits"], **{k: full[k] for k in keep}})
+
+
+def test_counts_are_exact(dsa):
+    """One token said thousands of times, one in the prompt alone, one only drafted; the same
+    bias twice: values exact in 32 bits."""
+    V, L = 3000, 5000
+    z = torch.zeros((1, 3, V), device="cuda")
+    z[..., 17], z[..., 18], z[..., 19], z[..., 20] = 2000.0, 8.0, -4.0, 5.0
+    history = torch.full((1, L), 17, dtype=torch.int32, device="cuda")
+    history[0, :100] = 18
+    one = lambda x: torch.tensor([x], device="cuda")  # noqa: E731
+    a = dict(logits=z, history=history, prompt_len=one(100).int(), draft=torch.tensor([[19, 19, 20]], device="cuda").int(),
+             repetition=one(2.0), frequency=one(0.25), presence=one(1.0),
+             bias_ids=torch.tensor([[20, 20, 17]], device="cuda").int(),
+             bias_values=torch.tensor([[1.0, 2.0, 0.5]], device="cuda"))
+    got = dsa.dsa_logits_probs(**a).cpu().double()
+    for j, (drafted, z19) in enumerate([(0, -4.0), (1, -8.0 - 0.25 - 1), (2, -8.0 - 0.5 - 1)]):
+        want = torch.zeros(V, dtype=torch.float64)
+        want[17] = 1000 - 4900 * 0.25 - 1 + 0.5
+        want[18], want[19], want[20] = 4.0, z19, 8.0
+        want = torch.softmax(want, -1)
+        assert float(((got[0, j] - want).abs() / want.clamp(min=1e-300)).nan_to_num(0)[want > 1e-30].max()) <= 2.0 ** -13
+
+
+@pytest.mark.parametrize("V", [40, 50000, 400000])
+def test_empty_rows_infinities_and_nan(dsa, V):
+    z = torch.randn((1, 8, V), generator=_gen(2), device="cuda")
+    mask = torch.full((1, 8, (V + 31) // 32), -1, dtype=torch.int32, device="cuda")
+    mask[0, 0] = 0                                            # nothing is allowed
+    z[0, 1] = -math.inf                                       # nothing is possible
+    z[0, 2, 3:9], z[0, 2, 30] = math.inf, math.nan            # six share the probability
+    z[0, 3, 5:] = math.nan
+    z[0, 4, 7] = math.inf
+    mask[0, 4, 0] = ~(1 << 7)                                 # the infinite one is not allowed
+    z[0, 5], z[0, 5, 11] = math.nan, -5.0                     # one entry is left
+    mask[0, 6] = 0
+    mask[0, 6, 1] = 1 << 2                                    # one entry is allowed
+    z[0, 7] = torch.finfo(torch.float32).min
+    z[0, 7, 9] = torch.finfo(torch.float32).max
+    got = _check(dsa, dict(logits=z, mask=mask))
+    assert bool((got[0, 0] == 0).all()) and bool((got[0, 1] == 0).all())
+    assert got[0, 2, 3:9].tolist() == [pytest.approx(1 / 6, rel=1e-6)] * 6 and got[0, 5, 11] == 1 and got[0, 6, 34] == 1
+    assert got[0, 7, 9] == 1
+    for T in (0.0, -1.0, math.nan):
+        hot = dsa.dsa_logits_probs(z, torch.tensor([T], device="cuda"), mask=mask).cpu()
+        assert bool((hot[0, :2] == 0).all())
+        assert hot[0, 2:].sum(-1).tolist() == [1.0] * 6
+        assert [int(r.argmax()) for r in hot[0, 2:]] == [3, int(z[0, 3, :5].argmax()), int(got[0, 4].argmax()), 11, 34, 9]
+
+
+@pytest.mark.parametrize("T", [1e-40, 1e-6, 1e6, math.inf])
+def test_extreme_temperatures(dsa, T):
+    z = torch.randn((1, 2, 777), generator=_gen(3), device="cuda")
+    z[0, 1, 5:9] = 50.0                                       # a tie
+    z[0, 0, 3] = -math.inf
+    got = dsa.dsa_logits_probs(z, torch.tensor([T], device="cuda")).cpu().double()
+    want = torch.softmax((z.cpu().double() - z.cpu().double().amax(-1, keepdim=True)) / float(torch.tensor(T)), -1)
+    if T == math.inf:
+        want = (z.cpu() > -math.inf).double()
+        want /= want.sum(-1, keepdim=True)
+    assert bool(((got - want).abs() <= 2.0 ** -14 * want + 1e-37).all())
+
+
+def test_greedy_ties_go_to_the_lowest_index(dsa):
+    for V in (64, 30000, 151552, 400001):
+        z = torch.zeros((1, 3, V), device="cuda")
+        z[0, 1, [V - 1, V // 2, V // 3]] = 4.0
+        z[0, 2, V - 1] = 1.0
+        hot = dsa.dsa_logits_probs(z, torch.zeros(1, device="cuda")).cpu()
+        assert [int(r.nonzero()[0, 0]) for r in hot[0]] == [0, V // 3, V - 1] and hot.sum() == 3
+
+
+def test_unaligned_rows_outputs_and_repeats(dsa):
+    """Rows that start at any element; the bytes around the output stay; two runs agree bit for bit."""
+    V = 20011
+    buffer = torch.randn(3 * V + 8, generator=_gen(4), device="cuda")
+    for lead in range(4):
+        for dtype in (torch.float32, torch.bfloat16):
+            z = buffer.to(dtype)[lead:lead + 3 * V].view(1, 3, V)
+            target = torch.full((3 * V + 8,), 9.0, device="cuda")
+            out = target[1 + lead:1 + lead + 3 * V].view(1, 3, V)
+            dsa.dsa_logits_probs(z, out=out)
+            want = torch.softmax(z.double(), -1)
+            assert bool(((out.double() - want).abs() <= 2.0 ** -13 * want).all())
+            assert bool((target[:1 + lead] == 9).all()) and bool((target[1 + lead + 3 * V:] == 9).all())
+            assert torch.equal(dsa.dsa_logits_probs(z), out)
+
+
+def test_a_captured_call_reads_the_present_history(dsa):
+    a = _inputs(2, 3, 60000, seed=5, hist=500, bias=10, mask=True)
+    out = torch.zeros((2, 3, 60000), device="cuda")
+    dsa.dsa_logits_probs(**a, out=out)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dsa.dsa_logits_probs(**a, out=out)
+    for seed in (6, 7):
+        b = _inputs(2, 3, 60000, seed=seed, hist=500, bias=10, mask=True)
+        for k in a:
+            a[k].copy_(b[k])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, dsa.dsa_logits_probs(**b))
+
+
+def test_binding_refusals(dsa):
+    z = torch.zeros((2, 1, 64), device="cuda")
+    ints = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")  # noqa: E731
+    for kw, err in [(dict(temperature=torch.zeros(3, device="cuda")), ValueError), (dict(history=ints(3, 4)), ValueError),
+                    (dict(history_len=ints(2)), ValueError), (dict(bias_ids=ints(2, 1)), ValueError),
+                    (dict(mask=ints(2, 1, 3)), ValueError), (dict(draft=ints(2, 1).long()), TypeError),
+                    (dict(out=torch.zeros((2, 1, 64), dtype=torch.bfloat16, device="cuda")), TypeError)]:
+        with pytest.raises(err):
+            dsa.dsa_logits_probs(z, **kw)
+    with pytest.raises(TypeError):
+        dsa.dsa_logits_probs(z.half())
+    assert dsa.dsa_logits_probs(z[:0]).shape == (0, 1, 64)
+
+
+def test_a_verify_step_over_a_paged_cache(dsa):
+    """The run of a step: rotate the queries, append the new rows, attend over the pages, turn
+    logits into probabilities, and verify the drafts with them."""
+    H, page, V, S, theta = 16, 64, 5000, 3, 1e6
+    new, ctx = [S + 1, S + 1], [500, 130]
+    batch = Batch(new, ctx, page, seed=8).fill()
+    f, m = frequencies(64, theta)
+    plan = dsa.dsa_rope_init(64, "interleaved", theta)
+    g = _gen(9)
+    x = torch.randn((batch.n, DQK), generator=g, device="cuda").to(torch.bfloat16)
+    gamma = torch.ones(DV, device="cuda", dtype=torch.bfloat16)
+    q = torch.randn((batch.n, H, DQK), generator=g, device="cuda").to(torch.bfloat16)
+    positions = torch.cat([torch.arange(c - k, c) for k, c in zip(new, ctx)]).cuda()
+    raw = q.clone()
+    dsa.dsa_rope(q[..., DV:], positions, plan, out=q[..., DV:])
+    want, size = rope(raw[..., DV:], positions, f, m, "interleaved")
+    assert bool(((q[..., DV:].double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -20 * size).all())
+    assert torch.equal(q[..., :DV], raw[..., :DV])
+    dsa.dsa_cache_append(x, gamma, 1e-6, plan, batch.cache, batch.table, batch.cu_q, batch.ctx_len)
+    out, lse = dsa.dsa_paged_attn(q, batch.cache, batch.table, batch.cu_q, batch.ctx_len, 1 / 24)
+    r_out, r_lse, r_size, reach = attention(batch, q, 1 / 24)
+    b_out, b_lse = attention_bounds(r_out, r_lse, r_size, reach, max(ctx))
+    assert bool(((out.double() - r_out).abs() <= b_out).all()) and bool(((lse.double() - r_lse).abs() <= b_lse).all())
+    # an output projection stands for the model between: logits of the two models
+    head = torch.randn((H * DV, V), generator=g, device="cuda") * 0.05
+    target = (out.float().view(2, S + 1, -1) @ head)[:, :S].contiguous()
+    drafter = (target + torch.randn(target.shape, generator=g, device="cuda")).contiguous()
+    history = torch.randint(0, V, (2, 500), generator=g, device="cuda", dtype=torch.int32)
+    kw = dict(history=history, history_len=torch.tensor(ctx, device="cuda").int() - S, repetition=torch.full((2,), 1.1, device="cuda"))
+    q_probs = dsa.dsa_logits_probs(drafter, **kw)
+    draft = torch.multinomial(q_probs.view(-1, V), 1, generator=g).view(2, S).int()
+    p = dsa.dsa_logits_probs(target, draft=draft, **kw)
+    ref, _ = probabilities(target, draft=draft, **kw)
+    assert bool(((p.cpu().double() - ref).abs() <= 2.0 ** -12 * ref + 1e-37).all())
+    u, u2 = torch.rand((2, S), generator=g, device="cuda"), torch.rand((2, S), generator=g, device="cuda")
+    alpha, accept, token, length = dsa.dsa_verify(p, q_probs, draft, u, u2)
+    torch.cuda.synchronize()
+    at = draft.long()[..., None]
+    assert torch.equal(accept.bool(), (u * q_probs.gather(2, at)[..., 0]) < p.gather(2, at)[..., 0])
+    assert torch.equal(token[accept.bool()], draft[accept.bool()])
+    for b in range(2):
+        flags = accept[b].tolist() + [0]
+        assert int(length[b]) == flags.index(0)
+    assert dsa.dsa_check_device_status() == 0

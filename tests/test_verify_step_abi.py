@@ -1,0 +1,154 @@
+"""Refusals of the entry points around the verify step and the rotary plan's frequencies.
+CPU only: no call here reaches a kernel launch."""
+import ctypes
+import math
+
+import pytest
+
+import sparse_long_context_score_b200 as dsa
+from verify_step import frequencies
+
+FAKE = ctypes.c_void_p(1 << 20)  # aligned, never dereferenced: every call below fails validation
+ODD = ctypes.c_void_p((1 << 20) + 1)
+TWO = ctypes.c_void_p((1 << 20) + 2)
+
+
+@pytest.fixture(scope="module")
+def L():
+    from sparse_long_context_score_b200 import build
+    build.build()
+    return dsa.lib()
+
+
+@pytest.mark.parametrize("layout", dsa.ROPE_LAYOUTS)
+@pytest.mark.parametrize("rot,theta,factor,orig", [(2, 10.0, 1.0, 0), (64, 1e4, 1.0, 0), (64, 1e6, 8.0, 16384),
+                                                   (128, 1e4, 40.0, 4096), (256, 1e4, 1.5, 1), (6, 5e5, 4.0, 100)])
+def test_plan_frequencies(L, layout, rot, theta, factor, orig):
+    plan = dsa.dsa_rope_init(rot, layout, theta, factor, orig)
+    f, m = frequencies(rot, theta, factor, orig)
+    assert plan.rot_dim == rot and plan.layout == dsa.ROPE_LAYOUTS.index(layout)
+    assert plan.mscale == ctypes.c_float(m).value
+    for i in range(128):
+        want = f[i] / (2 * math.pi) if i < rot // 2 else 0.0
+        assert abs(plan.turns[i] - want) <= 8 * 2.0 ** -53 * want
+
+
+def test_plan_refusals(L):
+    plan = dsa.RopePlan()
+    at = ctypes.addressof(plan)
+    assert L.dsa_rope_init(None, 64, 0, 1e4, 1.0, 0) == -1
+    for rot, layout, theta, factor, orig in [(0, 0, 1e4, 1.0, 0), (-2, 0, 1e4, 1.0, 0), (63, 0, 1e4, 1.0, 0),
+                                             (64, 2, 1e4, 1.0, 0), (64, 0, 1.0, 1.0, 0), (64, 0, math.nan, 1.0, 0),
+                                             (64, 0, math.inf, 1.0, 0), (64, 0, 1e4, 0.5, 0), (64, 0, 1e4, math.nan, 0),
+                                             (64, 0, 1e4, math.inf, 4096), (64, 0, 1e4, 4.0, 0)]:
+        assert L.dsa_rope_init(at, rot, layout, theta, factor, orig) == -1, (rot, layout, theta, factor, orig)
+    assert L.dsa_rope_init(at, 258, 0, 1e4, 1.0, 0) == -2
+    with pytest.raises(ValueError):
+        dsa.dsa_rope_init(64, "quarter")
+
+
+def test_rope_refusals(L):
+    plan = dsa.dsa_rope_init(64)
+    p = ctypes.addressof(plan)
+    ok = dict(x=FAKE, pos=FAKE, n=4, heads=2, dim=64, off=0, plan=p, dtype=0, xt=128, xh=64,
+              out=ctypes.c_void_p(1 << 24), ot=128, oh=64)
+
+    def call(**kw):
+        a = {**ok, **kw}
+        return L.dsa_rope(a["x"], a["pos"], a["n"], a["heads"], a["dim"], a["off"], a["plan"], a["dtype"], a["xt"], a["xh"],
+                          a["out"], a["ot"], a["oh"], None)
+
+    assert call(n=0) == 0                                      # nothing to do
+    for kw in [dict(x=None), dict(pos=None), dict(out=None), dict(plan=None), dict(n=-1), dict(heads=0), dict(dim=0),
+               dict(off=-1), dict(off=1), dict(dim=63), dict(x=ODD), dict(out=ODD), dict(pos=TWO), dict(xt=-128),
+               dict(oh=-64), dict(x=TWO, dtype=1),
+               dict(oh=63), dict(ot=127), dict(ot=0), dict(oh=0),  # heads of the output overlap
+               dict(out=FAKE, ot=256)]:                        # in place with other strides
+        assert call(**kw) == -1, kw
+    assert call(dtype=2) == -2
+    assert call(n=1 << 50) == -2
+    assert call(n=0, ot=64, oh=256) == 0                       # heads outermost
+    bad = dsa.RopePlan()
+    for rot, layout in [(0, 0), (63, 0), (258, 0), (64, 2), (64, -1)]:
+        bad.rot_dim, bad.layout = rot, layout
+        assert call(plan=ctypes.addressof(bad), dim=512, xt=1024, xh=512, ot=1024, oh=512) == -1
+
+
+def test_append_refusals(L):
+    plan = dsa.dsa_rope_init(64)
+    p = ctypes.addressof(plan)
+    wide = dsa.dsa_rope_init(128)
+    ok = dict(x=FAKE, stride=576, gamma=FAKE, eps=1e-6, plan=p, cache=FAKE, table=FAKE, cu=FAKE, ctx=FAKE, n=4, B=2, P=8,
+              page=64, most=4)
+
+    def call(**kw):
+        a = {**ok, **kw}
+        return L.dsa_cache_append(a["x"], a["stride"], a["gamma"], a["eps"], a["plan"], a["cache"], a["table"], a["cu"],
+                                  a["ctx"], a["n"], a["B"], a["P"], a["page"], a["most"], None)
+
+    assert call(n=0) == 0
+    for kw in [dict(x=None), dict(gamma=None), dict(plan=None), dict(cache=None), dict(table=None), dict(cu=None),
+               dict(ctx=None), dict(n=-1), dict(B=0), dict(P=0), dict(page=0), dict(most=0), dict(stride=575),
+               dict(stride=577), dict(stride=580), dict(x=TWO), dict(gamma=TWO), dict(cache=TWO), dict(table=TWO),
+               dict(eps=-1.0), dict(eps=math.nan)]:
+        assert call(**kw) == -1, kw
+    assert call(page=24) == -2
+    assert call(P=1 << 26, page=64) == -2
+    assert call(plan=ctypes.addressof(wide)) == -2
+
+
+def test_paged_attn_refusals(L):
+    ok = dict(q=FAKE, cache=FAKE, table=FAKE, cu=FAKE, ctx=FAKE, n=4, B=2, H=16, P=8, page=64, most=4, scale=0.1, out=FAKE,
+              lse=FAKE, ws=FAKE, size=1 << 40)
+
+    def call(**kw):
+        a = {**ok, **kw}
+        return L.dsa_paged_attn(a["q"], a["cache"], a["table"], a["cu"], a["ctx"], a["n"], a["B"], a["H"], a["P"], a["page"],
+                                a["most"], a["scale"], a["out"], a["lse"], a["ws"], a["size"], None)
+
+    assert call(n=0) == 0
+    for kw in [dict(q=None), dict(cache=None), dict(table=None), dict(cu=None), dict(ctx=None), dict(out=None), dict(n=-1),
+               dict(B=0), dict(H=0), dict(P=0), dict(page=0), dict(most=0), dict(q=TWO), dict(cache=TWO), dict(out=TWO),
+               dict(lse=TWO), dict(ctx=TWO), dict(scale=math.nan), dict(scale=math.inf)]:
+        assert call(**kw) == -1, kw
+    for kw in [dict(H=129), dict(page=40), dict(P=1 << 26), dict(n=1 << 30)]:
+        assert call(**kw) == -2, kw
+    for n, B, H in [(-1, 1, 1), (1, 0, 1), (1, 1, 0), (1, 1, 129), (1 << 30, 1, 16)]:
+        assert L.dsa_paged_workspace_size(n, B, H) == 0
+
+
+def test_logits_probs_refusals(L):
+    names = ["logits", "dtype", "B", "S", "V", "temperature", "repetition", "frequency", "presence", "history", "cap",
+             "history_len", "prompt_len", "draft", "bias_ids", "bias_values", "nbias", "mask", "p"]
+    ok = dict(logits=FAKE, dtype=1, B=2, S=3, V=100, p=FAKE, cap=0, nbias=0)
+
+    def call(**kw):
+        a = {**ok, **kw}
+        return L.dsa_logits_probs(*[a.get(k) for k in names], None)
+
+    assert call(B=0) == 0 and call(S=0) == 0
+    for kw in [dict(logits=None), dict(p=None), dict(B=-1), dict(S=-1), dict(V=0), dict(V=1 << 24), dict(cap=-1),
+               dict(nbias=-1), dict(nbias=1), dict(nbias=1, bias_ids=FAKE), dict(logits=TWO), dict(logits=ODD, dtype=0),
+               dict(p=TWO), dict(mask=TWO), dict(draft=TWO), dict(temperature=TWO), dict(B=1 << 20, S=1 << 20)]:
+        assert call(**kw) == -1, kw
+    assert call(dtype=2) == -2
+    assert call(cap=1 << 30, history=FAKE) == -2
+
+
+def test_binding_refuses_cpu_tensors():
+    import torch
+    plan = dsa.dsa_rope_init(64)
+    bf = torch.bfloat16
+    i32 = torch.int32
+    with pytest.raises(ValueError):
+        dsa.dsa_rope(torch.zeros(2, 1, 64, dtype=bf), torch.zeros(2, dtype=torch.int64), plan)
+    with pytest.raises(ValueError):
+        dsa.dsa_cache_append(torch.zeros(1, 576, dtype=bf), torch.zeros(512, dtype=bf), 1e-6, plan,
+                             torch.zeros(1, 16, 576, dtype=bf), torch.zeros(1, 1, dtype=i32), torch.zeros(2, dtype=i32),
+                             torch.zeros(1, dtype=i32))
+    with pytest.raises(ValueError):
+        dsa.dsa_paged_attn(torch.zeros(1, 16, 576, dtype=bf), torch.zeros(1, 16, 576, dtype=bf),
+                           torch.zeros(1, 1, dtype=i32), torch.zeros(2, dtype=i32), torch.zeros(1, dtype=i32), 0.1,
+                           ws=torch.zeros(256, dtype=torch.uint8))
+    with pytest.raises(ValueError):
+        dsa.dsa_logits_probs(torch.zeros(1, 1, 32))
