@@ -218,28 +218,32 @@ DecodeEvents* decode_events() {
   return &d;
 }
 
-// The error words of the indexer, the attention and the top-k, in that order.
+// The error words of the indexer, the attention, the top-k and the paged attention, in that
+// order.
 struct ErrorWords {
-  int code[3] = {0, 0, 0};
-  int first() const { return code[0] ? code[0] : code[1] ? code[1] : code[2]; }
-  // a wait that ran out (indexer, attention) is a timeout; a broken top-k invariant a
+  int code[4] = {0, 0, 0, 0};
+  int first() const { return code[0] ? code[0] : code[1] ? code[1] : code[2] ? code[2] : code[3]; }
+  // a wait that ran out (indexer, attentions) is a timeout; a broken top-k invariant a
   // device error
-  dsa_status status() const { return (code[0] || code[1]) ? DSA_ERR_TIMEOUT : code[2] ? DSA_ERR_DEVICE : DSA_OK; }
+  dsa_status status() const {
+    return (code[0] || code[1] || code[3]) ? DSA_ERR_TIMEOUT : code[2] ? DSA_ERR_DEVICE : DSA_OK;
+  }
 };
 
 // Reads the error words on `stream` (the caller has synchronised whatever it wants
 // covered) and, with `clear`, resets the ones that are set.
 cudaError_t read_error_words(cudaStream_t stream, bool clear, ErrorWords* w) {
-  int* p[3] = {nullptr, nullptr, nullptr};
+  int* p[4] = {nullptr, nullptr, nullptr, nullptr};
   cudaError_t e;
   if ((e = indexer_error_word(&p[0])) != cudaSuccess) return e;
   if ((e = attn_error_word(&p[1])) != cudaSuccess) return e;
   if ((e = topk_error_word(&p[2])) != cudaSuccess) return e;
-  for (int i = 0; i < 3; ++i)
+  if ((e = paged_error_word(&p[3])) != cudaSuccess) return e;
+  for (int i = 0; i < 4; ++i)
     if ((e = cudaMemcpyAsync(&w->code[i], p[i], sizeof(int), cudaMemcpyDeviceToHost, stream)) != cudaSuccess) return e;
   if ((e = cudaStreamSynchronize(stream)) != cudaSuccess) return e;
   if (clear) {
-    for (int i = 0; i < 3; ++i)
+    for (int i = 0; i < 4; ++i)
       if (w->code[i] && (e = cudaMemsetAsync(p[i], 0, sizeof(int), stream)) != cudaSuccess) return e;
     if ((e = cudaStreamSynchronize(stream)) != cudaSuccess) return e;
   }

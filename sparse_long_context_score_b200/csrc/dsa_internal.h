@@ -164,6 +164,7 @@ cudaError_t launch_cache_append(const uint16_t* x, long long x_stride, const uin
 size_t paged_attn_workspace_bytes(long long n, int B, int H);
 cudaError_t launch_paged_attn(const uint16_t* q, const uint16_t* cache, const PagedBatch& pb, int H, float scale,
                               uint16_t* out, float* lse, void* workspace, cudaStream_t stream);
+cudaError_t paged_error_word(int** p);
 
 // logits to probabilities (probs.cu); null pointers: no such step
 struct ProbsArgs {
