@@ -585,7 +585,7 @@ dsa_status dsa_cache_append(const uint16_t* x, long long x_stride, const uint16_
 
 size_t dsa_paged_workspace_size(int n, int B, int H) {
   if (n < 0 || B <= 0 || H <= 0 || H > 128 || (long long)n * H > 0x7FFFFFFFLL) return 0;
-  return paged_attn_workspace_bytes(n, B, H);
+  return paged_attn_workspace_bytes();
 }
 
 dsa_status dsa_paged_attn(const uint16_t* q, const uint16_t* cache, const int32_t* table, const int32_t* cu_q,
@@ -598,7 +598,7 @@ dsa_status dsa_paged_attn(const uint16_t* q, const uint16_t* cache, const int32_
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4)) return DSA_ERR_INVALID_ARG;
   if (H > 128 || (long long)n * H > 0x7FFFFFFFLL) return DSA_ERR_UNSUPPORTED;
   if (n == 0) return DSA_OK;
-  const size_t need = paged_attn_workspace_bytes(n, B, H);
+  const size_t need = paged_attn_workspace_bytes();
   if (need == 0) return cuda_status(cudaErrorInvalidDevice);
   if (!workspace || workspace_bytes < need || !aligned(workspace, 256)) return DSA_ERR_WORKSPACE;
   const PagedBatch pb{table, cu_q, ctx_len, n, B, max_pages, num_pages, page_size};

@@ -161,7 +161,7 @@ cudaError_t launch_cache_append(const uint16_t* x, long long x_stride, const uin
 
 // chunk attention over a paged cache (paged_attn.cu); 0 bytes when the device cannot be
 // queried
-size_t paged_attn_workspace_bytes(long long n, int B, int H);
+size_t paged_attn_workspace_bytes();
 cudaError_t launch_paged_attn(const uint16_t* q, const uint16_t* cache, const PagedBatch& pb, int H, float scale,
                               uint16_t* out, float* lse, void* workspace, cudaStream_t stream);
 cudaError_t paged_error_word(int** p);

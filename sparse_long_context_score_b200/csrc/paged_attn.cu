@@ -9,8 +9,7 @@
 // (query tile, key tile) pairs of the whole batch, in order, are dealt out in equal
 // contiguous shares, one a CTA and one CTA an SM: a long context is split over CTAs when
 // there are few query rows, and a CTA works through many query tiles when there are many.
-// paged_plan_kernel finds where each share starts (lengths are read on the device);
-// a query tile that one CTA covers is written directly, the parts of one that crosses a
+// The lengths are read on the device, and every CTA finds its own share.  A query tile that one CTA covers is written directly, the parts of one that crosses a
 // share's border go to the workspace in 32 bits and paged_combine_kernel joins them in the
 // CTAs' order (no atomics: the result does not depend on timing).
 //
@@ -45,12 +44,14 @@ constexpr int kStageBytes = kBlocks * kBlockBytes;  // 147456
 // P of a tile (64 rows x 128 keys bf16, two 8 KB halves of 64 keys) is written over the
 // tile's rotary block, which only S reads
 constexpr int kPBlock = kDv / 64;
+constexpr int kMaxCtas = 256;                    // shares at most (one an SM)
 constexpr int kSegs = 4;                         // query tile segments in flight
 
 constexpr int kLoadWarp = 0, kMmaWarp = 1, kQueryWarp = 2, kWalkWarp = 3, kSoftmaxWarp0 = 4;
 constexpr int kSoftmaxThreads = 256;             // eight warps: two per TMEM lane quarter
 constexpr int kThreadsP = kSoftmaxWarp0 * 32 + kSoftmaxThreads;  // 384
 constexpr float kRescaleLog2 = 8.f;
+constexpr int kPrefetchTiles = 4;
 
 // One CTA's part of a query tile.
 struct Segment {
@@ -61,16 +62,20 @@ struct Segment {
   int k0, k1;    // key tiles
   int seen0;     // cached rows that the sequence's first new token sees
   int limit;     // cached rows of the sequence
+  int tiles;     // query tiles of the sequence
   int part;      // workspace slot of this part of the tile; -1: the tile is whole
 };
 
-// Where a CTA's share starts: key tile k0 of query tile `tile` of sequence b.
+// Where a CTA's share starts: key tile k0 of query tile `tile` of sequence b (-1: nowhere),
+// and its key tiles.
 struct Share {
-  int b, tile, k0;
+  int b, tile, k0, keys;
 };
-struct Plan {
-  int per_cta;  // key tiles of a share
-  int pad[3];
+// A query tile that CTA g begins and later CTAs go on with, for the combine.
+struct Join {
+  int row0, nrows;  // as in Segment
+  int parts;        // CTAs g .. g + parts - 1 hold one each; 0: none
+  int pad;
 };
 
 constexpr int kOffQ = 0;
@@ -79,11 +84,14 @@ constexpr int kOffMax = kOffStage + kStageBytes;     // [2][64] f32: a tile's ma
 constexpr int kOffAlpha = kOffMax + 2 * 64 * 4;      // [64] f32
 constexpr int kOffL = kOffAlpha + 64 * 4;            // [2][64] f32
 constexpr int kOffM = kOffL + 2 * 64 * 4;            // [64] f32
-constexpr int kOffVote = kOffM + 64 * 4;             // [8] u32, one per softmax warp
-constexpr int kOffBad = kOffVote + 8 * 4;            // u32: 16-row groups of the tile that are not there
-constexpr int kOffSeg = kOffBad + 32;
+constexpr int kOffVote = kOffM + 64 * 4;             // [4] u32: a lane quarter has a row to rescale
+constexpr int kOffOver = kOffVote + 16;              // u32: number of the last guessed tile that exceeded the maximum
+constexpr int kOffBad = kOffOver + 16;               // u32: 16-row groups of the tile that are not there
+constexpr int kOffShare = kOffBad + 16;
+constexpr int kOffSum = kOffShare + 16;              // [12] i64: per warp
+constexpr int kOffSeg = kOffSum + kThreadsP / 32 * 8;
 constexpr int kOffBar = kOffSeg + kSegs * (int)sizeof(Segment) + 16;
-constexpr int kNumBars = kBlocks + 5 + 2 * kSegs + 8;
+constexpr int kNumBars = 10 + 2 * kSegs + 8;
 constexpr int kOffTmem = kOffBar + kNumBars * 8;
 constexpr int kSmemP = kOffTmem + 16 + 1024;         // + alignment slack
 static_assert(kOffBar % 8 == 0, "barrier alignment");
@@ -95,106 +103,61 @@ constexpr int kTmemCols = 512;
 
 constexpr int kPartFloats = kRows * kDv;             // one part's [64][512] sums
 
-// The plan and the parts are read behind griddepcontrol.wait by volatile loads: a load that
-// the compiler may take for one of constant data could move above the wait.
-__device__ __forceinline__ Share load_share(const Share* p) {
-  const volatile int* v = reinterpret_cast<const volatile int*>(p);
-  return Share{v[0], v[1], v[2]};
+constexpr uint32_t kMinusInf = 0xFF800000u;
+
+// 2^x; results below the normal range become zero
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-// rows of a sequence's query tile, and the key tiles that it visits (at least one, so that
-// rows which see nothing are written too)
+__device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+// Query rows of a sequence and the cached rows that they see.
 struct SequenceWork {
   int tiles, rows, seen0, limit;
 };
 __device__ __forceinline__ SequenceWork sequence_work(const PagedBatch& p, int b, int H) {
-  const int q0 = p.cu_q[b], nb = max(min(p.cu_q[b + 1], p.n) - q0, 0);
-  const int full = p.cu_q[b + 1] - q0;
+  const int q0 = p.cu_q[b], q1 = p.cu_q[b + 1];
   SequenceWork w;
-  w.rows = q0 < 0 ? 0 : nb * H;
+  w.rows = q0 < 0 ? 0 : max(min(q1, p.n) - q0, 0) * H;
   w.tiles = (w.rows + kRows - 1) / kRows;
-  const long long most = (long long)p.max_pages * p.page_size;
-  w.limit = (int)max(0LL, min((long long)p.ctx_len[b], most));
-  w.seen0 = p.ctx_len[b] - full + 1;
+  w.limit = (int)max(0LL, min((long long)p.ctx_len[b], (long long)p.max_pages * p.page_size));
+  w.seen0 = p.ctx_len[b] - (q1 - q0) + 1;
   return w;
 }
+// Key tiles that a query tile visits: those its last row sees, and at least one, so that
+// rows which see nothing are written too.
 __device__ __forceinline__ int tile_keys(const SequenceWork& w, int tile, int H) {
   const int last = min(kRows * (tile + 1), w.rows) - 1;
   const int seen = min(w.seen0 + last / H, w.limit);
   return max(1, (seen + kKeys - 1) / kKeys);
 }
-
-// Deals the (query tile, key tile) pairs out: one warp sums a sequence's pairs, a scan over
-// the sequences gives the total, and a second pass over the tiles notes where each share
-// starts.
-__global__ void __launch_bounds__(1024) paged_plan_kernel(PagedBatch p, int H, int ctas, long long* __restrict__ before,
-                                                          Plan* __restrict__ plan, Share* __restrict__ shares) {
-  __shared__ long long s_warp[32];
-  __shared__ long long s_total;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  grid_dep_launch();
-  for (int g = threadIdx.x; g < ctas; g += 1024) shares[g].b = -1;
-  for (int b = warp; b < p.B; b += 32) {
-    const SequenceWork w = sequence_work(p, b, H);
-    long long sum = 0;
-    for (int i = lane; i < w.tiles; i += 32) sum += tile_keys(w, i, H);
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    if (lane == 0) before[b] = sum;
-  }
-  if (threadIdx.x == 0) s_total = 0;
-  __syncthreads();
-  for (int b0 = 0; b0 < p.B; b0 += 1024) {  // exclusive sums over the sequences
-    const int b = b0 + threadIdx.x;
-    const long long own = b < p.B ? before[b] : 0;
-    long long v = own;
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long u = __shfl_up_sync(0xFFFFFFFFu, v, o);
-      if (lane >= o) v += u;
-    }
-    if (lane == 31) s_warp[warp] = v;
-    __syncthreads();
-    if (warp == 0) {
-      long long t = s_warp[lane];
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long u = __shfl_up_sync(0xFFFFFFFFu, t, o);
-        if (lane >= o) t += u;
-      }
-      s_warp[lane] = t;
-    }
-    __syncthreads();
-    const long long base = s_total;
-    if (b < p.B) before[b] = base + (warp ? s_warp[warp - 1] : 0) + v - own;
-    __syncthreads();
-    if (threadIdx.x == 0) s_total = base + s_warp[31];
-    __syncthreads();
-  }
-  const long long total = s_total;
-  const int per = (int)max(1LL, (total + ctas - 1) / ctas);
-  if (threadIdx.x == 0) plan->per_cta = per;
-  for (int b = warp; b < p.B; b += 32) {
-    const SequenceWork w = sequence_work(p, b, H);
-    long long at = before[b];
-    for (int i0 = 0; i0 < w.tiles; i0 += 32) {
-      const int i = i0 + lane, k = i < w.tiles ? tile_keys(w, i, H) : 0;
-      int v = k;
-      for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xFFFFFFFFu, v, o);
-        if (lane >= o) v += u;
-      }
-      const long long first = at + v - k;  // the tile's pairs are [first, first + k)
-      for (long long g = (first + per - 1) / per; g * per < first + k; ++g) {
-        Share s{b, i, (int)(g * per - first)};
-        shares[g] = s;
-      }
-      at += __shfl_sync(0xFFFFFFFFu, v, 31);
+// Key tiles that the query tiles before `tile` visit.  Tiles see ever more rows, so each key
+// tile m is visited from one query tile on: the first whose last row, of token
+// (64 (i + 1) - 1) / H, sees more than 128 m rows.
+__device__ __forceinline__ long long keys_before(const SequenceWork& w, int tile, int H) {
+  if (tile <= 0) return 0;
+  long long sum = 0;
+  const int whole = min(tile, w.tiles - 1);  // all but the last tile have 64 rows
+  if (whole > 0) {
+    const int first = tile_keys(w, 0, H), last = tile_keys(w, whole - 1, H);
+    sum = (long long)whole * first;
+    for (int m = first; m < last; ++m) {
+      const long long token = (long long)kKeys * m + 1 - w.seen0;  // the first that sees key tile m
+      const long long i = max(0LL, (token * H + kRows) / kRows - 1);  // (64 (i + 1) - 1) / H >= token
+      if (i < whole) sum += whole - i;
     }
   }
+  return tile == w.tiles ? sum + tile_keys(w, w.tiles - 1, H) : sum;
 }
 
 __global__ void __launch_bounds__(kThreadsP, 1)
-paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap cmap, PagedBatch p, int H,
-                  int box, float scale_log2, const Plan* plan, const Share* shares, uint16_t* out, float* lse, float* parts,
-                  float2* part_ml, int* err) {
+paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap cmap,
+                  const __grid_constant__ CUtensorMap rmap, PagedBatch p, int H, int box, float scale_log2, uint32_t negate, const uint16_t* cache, uint16_t* out, float* lse, Join* joins, float* parts, float2* part_ml, int* err) {
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   const uint32_t sbase = smem_u32(smem);
@@ -204,15 +167,17 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
   float* s_l = reinterpret_cast<float*>(smem + kOffL);
   float* s_m = reinterpret_cast<float*>(smem + kOffM);
   volatile uint32_t* s_vote = reinterpret_cast<volatile uint32_t*>(smem + kOffVote);
+  volatile uint32_t* s_over = reinterpret_cast<volatile uint32_t*>(smem + kOffOver);
   volatile uint32_t* s_bad = reinterpret_cast<volatile uint32_t*>(smem + kOffBad);
+  Share* s_share = reinterpret_cast<Share*>(smem + kOffShare);
   Segment* s_seg = reinterpret_cast<Segment*>(smem + kOffSeg);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + kOffTmem);
   const uint32_t bar0 = sbase + kOffBar;
-  auto full_bar = [&](int i) { return bar0 + 8u * i; };                          // block i has landed
-  auto free_bar = [&](int i) { return bar0 + 8u * (kBlocks + i); };              // blocks 2i, 2i + 1 (i < 4), block 8
-  auto segfull_bar = [&](int i) { return bar0 + 8u * (kBlocks + 5 + i); };
-  auto segfree_bar = [&](int i) { return bar0 + 8u * (kBlocks + 5 + kSegs + i); };
-  const uint32_t bars = bar0 + 8u * (kBlocks + 5 + 2 * kSegs);
+  auto full_bar = [&](int i) { return bar0 + 8u * i; };                 // blocks 2i, 2i + 1 (i < 4), block 8 landed
+  auto free_bar = [&](int i) { return bar0 + 8u * (5 + i); };           // ... are free
+  auto segfull_bar = [&](int i) { return bar0 + 8u * (10 + i); };
+  auto segfree_bar = [&](int i) { return bar0 + 8u * (10 + kSegs + i); };
+  const uint32_t bars = bar0 + 8u * (10 + 2 * kSegs);
   const uint32_t qfull_bar = bars, qfree_bar = bars + 8, sfull_bar = bars + 16, pfull_bar = bars + 24;
   const uint32_t ofull_bar = bars + 32, ofree_bar = bars + 40, grp_bar = bars + 48, done_bar = bars + 56;
 
@@ -220,8 +185,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
   const int cta = blockIdx.x;
   grid_dep_launch();  // the combine may be scheduled; it waits on the device for this grid
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kBlocks; ++i) mbar_init(full_bar(i), 1);
-    for (int i = 0; i < 5; ++i) mbar_init(free_bar(i), 1);
+    for (int i = 0; i < 5; ++i) {
+      mbar_init(full_bar(i), 1);
+      mbar_init(free_bar(i), 1);
+    }
     for (int i = 0; i < kSegs; ++i) {
       mbar_init(segfull_bar(i), 1);
       mbar_init(segfree_bar(i), 3 + kSoftmaxThreads / 32);  // load, MMA, query and softmax warps
@@ -229,16 +196,69 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
     mbar_init(qfull_bar, 1);
     mbar_init(qfree_bar, 1);
     mbar_init(sfull_bar, 1);
-    mbar_init(pfull_bar, kSoftmaxThreads);
+    mbar_init(pfull_bar, kSoftmaxThreads / 32);
     mbar_init(ofull_bar, 1);
-    mbar_init(ofree_bar, kSoftmaxThreads);
-    mbar_init(grp_bar, kSoftmaxThreads);
+    mbar_init(ofree_bar, kSoftmaxThreads / 32);
+    mbar_init(grp_bar, kSoftmaxThreads / 32);
     mbar_init(done_bar, 1);
+    *s_over = 0u;
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
     tmem_alloc(smem_u32(s_tmem), kTmemCols);
     tmem_relinquish();
+  }
+  // Where this CTA's share starts: every CTA sums the batch's key tiles, a thread a sequence.
+  // (A launch of its own for that, read by all CTAs, took 6 us more at 8 sequences.)
+  {
+    long long* s_sum = reinterpret_cast<long long*>(smem + kOffSum);
+    long long total = 0, own = 0, before = 0;
+    SequenceWork w{0, 0, 0, 0};
+    auto scan = [&](int b0) {  // keys of sequence b0 + threadIdx.x, the sum before it, the sum of all 384
+      const int b = b0 + threadIdx.x;
+      own = 0;
+      if (b < p.B) {
+        w = sequence_work(p, b, H);
+        own = keys_before(w, w.tiles, H);
+      }
+      long long v = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xFFFFFFFFu, v, o);
+        if (lane >= o) v += u;
+      }
+      __syncthreads();
+      if (lane == 31) s_sum[warp] = v;
+      __syncthreads();
+      long long all = 0, mine = 0;
+#pragma unroll
+      for (int i = 0; i < kThreadsP / 32; ++i) {
+        if (i == warp) mine = all;
+        all += s_sum[i];
+      }
+      before = mine + v - own;
+      return all;
+    };
+    for (int b0 = 0; b0 < p.B; b0 += kThreadsP) total += scan(b0);
+    const long long per = max(1LL, (total + gridDim.x - 1) / gridDim.x), start = per * cta;
+    if (threadIdx.x == 0) *s_share = Share{-1, 0, 0, 0};
+    long long base = 0;
+    for (int b0 = 0; b0 < p.B; b0 += kThreadsP) {
+      long long all = total;
+      if (p.B > kThreadsP) all = scan(b0);
+      else __syncthreads();
+      const long long at = start - base - before;
+      if (at >= 0 && at < own) {
+        int lo = 0, hi = w.tiles - 1;  // the last tile with keys_before <= at
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) / 2;
+          if (keys_before(w, mid, H) <= at) lo = mid;
+          else hi = mid - 1;
+        }
+        *s_share = Share{b0 + (int)threadIdx.x, lo, (int)(at - keys_before(w, lo, H)), (int)min(per, 0x7FFFFFFFLL)};
+      }
+      base += all;
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -266,9 +286,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
     if (lane == 0) {
       tma_prefetch(&qmap);
       tma_prefetch(&cmap);
-      grid_dep_wait();  // the plan (and with it all that was written before it)
-      const Share first = load_share(shares + cta);
-      int left = *reinterpret_cast<const volatile int*>(&plan->per_cta), b = first.b, tile = first.tile, k0 = first.k0;
+      tma_prefetch(&rmap);
+      const Share first = *s_share;
+      int left = first.keys, b = first.b, tile = first.tile, k0 = first.k0;
+      Join join{0, 0, 0, 0};
       SequenceWork w{0, 0, 0, 0};
       if (b >= 0) w = sequence_work(p, b, H);
       for (int i = 0;; ++i) {
@@ -289,7 +310,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
           s.k1 = min(keys, k0 + left);
           s.seen0 = w.seen0;
           s.limit = w.limit;
+          s.tiles = w.tiles;
           s.part = k0 > 0 ? 2 * cta : s.k1 < keys ? 2 * cta + 1 : -1;
+          if (k0 == 0 && s.k1 < keys) join = Join{s.row0, s.nrows, 1 + (keys - s.k1 + first.keys - 1) / first.keys, 0};
           left -= s.k1 - k0;
           k0 = 0;
           ++tile;
@@ -299,6 +322,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
         mbar_arrive(segfull_bar(at));
         if (s.b < 0) break;
       }
+      joins[cta] = join;
     }
     __syncwarp();
   } else if (warp == kQueryWarp) {
@@ -309,7 +333,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
       if (!warp_wait(qfree_bar, (i & 1) ^ 1, 43)) break;
       if (lane == 0) {
         mbar_arrive_expect_tx(qfull_bar, kQBytes);
-        for (int kb = 0; kb < kBlocks; ++kb) tma_load_2d(sQ + kb * kQBlockBytes, &qmap, qfull_bar, 64 * kb, s.row0);
+        tma_load_3d(sQ, &qmap, qfull_bar, 0, s.row0, 0);
       }
       issued = i + 1;
     }
@@ -320,7 +344,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
     // lane l brings rows [box l, box (l + 1)) of a tile, which lie in one page
     const int boxes = kKeys / box;
     Segment s;
-    int it = 0, posted = 0;  // key tiles, and blocks asked for
+    int it = 0;
     bool ok = true;
     while (ok && next_segment(s)) {
       const int32_t* table = p.table + (size_t)s.b * p.max_pages;
@@ -332,53 +356,82 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
         const int page = table[i];
         return page >= 0 && page < p.num_pages ? page * p.page_size + (int)(pos - i * p.page_size) : -1;
       };
-      int row = page_row(s.k0);
+      int row = page_row(s.k0), next = page_row(s.k0 + 1);
+      // A context that few query tiles read comes from HBM: its tiles are brought into L2 two
+      // ahead, so that the stream goes on while the blocks of shared memory are in use.  (By
+      // plain prefetches: the copy engine takes as long for a prefetched tile as for a loaded
+      // one.)
+      const bool from_hbm = s.tiles <= kPrefetchTiles;
+      auto prefetch = [&](int r) {
+        if (!from_hbm) return;
+#pragma unroll
+        for (int i = 0; i < kKeys / 32; ++i) {
+          const int y = 32 * i + lane, base = __shfl_sync(0xFFFFFFFFu, r, y / box);
+          if (base < 0) continue;
+          const char* line = reinterpret_cast<const char*>(cache) + ((size_t)base + y % box) * (kDqk * 2);
+#pragma unroll
+          for (int j = 0; j < kBlocks; ++j) asm volatile("prefetch.global.L2 [%0];" ::"l"(line + 128 * j));
+        }
+      };
+      prefetch(next);
       for (int k = s.k0; k < s.k1; ++k, ++it) {
-        const int ahead = page_row(k + 1);  // in flight while this tile is waited for
+        const int ahead = page_row(k + 2);
         const uint32_t there = __ballot_sync(0xFFFFFFFFu, row >= 0);
         uint32_t bad = 0;  // per 16 rows
         for (int i = 0; i < kKeys / 16; ++i) bad |= ((there >> (i * 16 / box)) & 1u ? 0u : 1u) << i;
-#pragma unroll 1
-        for (int kb = 0; kb < kBlocks; ++kb) {
-          if ((kb & 1) == 0) {
-            ok = warp_wait(free_bar(kb >> 1), (it & 1) ^ 1, 44);
-            if (!ok) break;
+        const int y = row >= 0 ? row : 0;
+#pragma unroll
+        for (int i = 0; i < 5; ++i) {  // blocks 2i, 2i + 1; the rotary block alone
+          ok &= mbar_wait(free_bar(i), (it & 1) ^ 1, err, 44);
+          if (i == 0) {  // the tile before is read up to its last block by then
+            if (lane == 0) *s_bad = bad;
+            if (lane < 5) mbar_arrive_expect_tx(full_bar(lane), lane < 4 ? 2 * kBlockBytes : kBlockBytes);
+            __syncwarp();
           }
-          if (lane == 0) {
-            if (kb == 0) *s_bad = bad;
-            mbar_arrive_expect_tx(full_bar(kb), kBlockBytes);
+          const uint32_t dst = sStage + 2 * i * kBlockBytes + lane * box * 128;
+          if (i == 4) {
+            if (lane < boxes) tma_load_3d(dst, &rmap, full_bar(4), 0, y, 8);
+          } else if (box == kKeys) {
+            if (lane == 0) tma_load_3d(dst, &cmap, full_bar(i), 0, y, 2 * i);
+          } else if (lane < boxes) {
+            // (a box of two blocks would put the second one right behind the box's rows)
+            tma_load_3d(dst, &rmap, full_bar(i), 0, y, 2 * i);
+            tma_load_3d(dst + kBlockBytes, &rmap, full_bar(i), 0, y, 2 * i + 1);
           }
-          __syncwarp();
-          if (lane < boxes)
-            tma_load_2d(sStage + kb * kBlockBytes + lane * box * 128, &cmap, full_bar(kb), 64 * kb, row >= 0 ? row : 0);
-          ++posted;
         }
+        ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
-        row = ahead;
+        prefetch(ahead);
+        row = next;
+        next = ahead;
       }
     }
     // nothing in flight on the way out: every block that was asked for has landed
-    if (lane == 0)
-      for (int kb = 0; kb < kBlocks && kb < posted; ++kb) mbar_wait_drain(full_bar(kb), ((posted - 1 - kb) / kBlocks) & 1);
+    if (lane == 0 && it + !ok > 0)
+      for (int i = 0; i < 5; ++i) mbar_wait_drain(full_bar(i), (it + !ok - 1) & 1);
     __syncwarp();
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------------ tensor core
     const bool leader = elect_one();
-    constexpr uint32_t idS = idesc_bf16_f32(kRows, kKeys);          // Q (K-major) x K (K-major)
+    // Q (K-major) x K (K-major); a negative scale negates Q, so that the largest S is the
+    // largest logit
+    const uint32_t idS = idesc_bf16_f32(kRows, kKeys) | negate;
     constexpr uint32_t idPV = idesc_bf16_f32(128, kRows, true, false);  // V^T (M-major) x P (K-major)
     const uint64_t dq = sdesc_kmajor_sw128(sQ), dk = sdesc_kmajor_sw128(sStage);
     const uint64_t dv = sdesc_mnmajor_sw128(sStage, kBlockBytes, 1024);
     const uint64_t dp = sdesc_kmajor_sw128(sStage + kPBlock * kBlockBytes);
     Segment s;
     int it = 0;
+    uint32_t pp = 0;  // phases of pfull seen
     bool ok = true;
     for (int i = 0; ok && next_segment(s); ++i) {
       ok = warp_wait(qfull_bar, i & 1, 45);
       for (int k = s.k0; ok && k < s.k1; ++k, ++it) {
-#pragma unroll 1
-        for (int kb = 0; ok && kb < kBlocks; ++kb) {
-          ok = warp_wait(full_bar(kb), it & 1, 46);
-          if (!ok) break;
+        // (unrolled, so that descriptors are a base and a constant: an issue loop that adds
+        // them up at run time is slower than the tensor core)
+#pragma unroll
+        for (int kb = 0; kb < kBlocks; ++kb) {
+          if (kb % 2 == 0) ok &= mbar_wait(full_bar(kb / 2), it & 1, err, 46);
           if (kb == 0) tc_fence_after();
           if (leader) {
 #pragma unroll
@@ -388,6 +441,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
           }
           __syncwarp();
         }
+        ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
         if (leader) {
           mma_commit(sfull_bar);
@@ -396,11 +450,17 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
         __syncwarp();
         // the epilogue of the segment before has read O
         if (k == s.k0) ok = warp_wait(ofree_bar, (i & 1) ^ 1, 47);
-        ok = ok && warp_wait(pfull_bar, it & 1, 48);
+        ok = ok && warp_wait(pfull_bar, pp++ & 1, 48);
         if (!ok) break;
+        if (k > s.k0 && k + 1 < s.k1 && *s_over == (uint32_t)it + 1u) {  // a wrong guess: the tile's weights again
+          __syncwarp();
+          if (lane == 0) mbar_arrive(sfull_bar);
+          ok = warp_wait(pfull_bar, pp++ & 1, 57);
+          if (!ok) break;
+        }
         tc_fence_after();
         if (leader) {
-#pragma unroll 1
+#pragma unroll
           for (int mb = 0; mb < 4; ++mb) {
 #pragma unroll
             for (int ks = 0; ks < kKeys / 16; ++ks)
@@ -429,127 +489,159 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
     const int rA = 16 * quarter + (lane >> 2), rB = rA + 8;
     const uint32_t lane_addr = (uint32_t)(32 * quarter) << 16;
     const int st = threadIdx.x - 32 * kSoftmaxWarp0;  // 0 .. 255
-    unsigned char* pbase = smem + kOffStage + kPBlock * kBlockBytes + half * (kBlockBytes / 2);
-    unsigned char* prowA = pbase + rA * 128 + 4 * c4;
-    unsigned char* prowB = pbase + rB * 128 + 4 * c4;
+    const uint32_t pbase = sStage + kPBlock * kBlockBytes + half * (kBlockBytes / 2);
+    const uint32_t prowA = pbase + rA * 128 + 4 * c4, prowB = pbase + rB * 128 + 4 * c4;
     uint32_t grp_phase = 0;
     auto group_sync = [&](int code) {
-      mbar_arrive(grp_bar);
-      const bool ok = mbar_wait(grp_bar, grp_phase, err, code);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(grp_bar);
+      const bool ok = warp_wait(grp_bar, grp_phase, code);
       grp_phase ^= 1;
       return ok;
     };
     Segment s;
-    int it = 0;
+    uint32_t sp = 0;    // phases of sfull seen
+    uint32_t tiles = 0;  // key tiles weighted, this CTA's first being number 1
     bool ok = true;
     for (int i = 0; ok && next_segment(s); ++i) {
       // cached rows that this thread's query rows see
       const int seenA = rA < s.nrows ? max(0, min(s.seen0 + (s.tile_row + rA) / H, s.limit)) : 0;
       const int seenB = rB < s.nrows ? max(0, min(s.seen0 + (s.tile_row + rB) / H, s.limit)) : 0;
-      float mA = -INFINITY, mB = -INFINITY, lA = 0.f, lB = 0.f;
-      for (int k = s.k0; k < s.k1; ++k, ++it) {
-        ok = warp_wait(full_bar(0), it & 1, 50) && warp_wait(sfull_bar, it & 1, 51);
+      float mA = -INFINITY, mB = -INFINITY, lA = 0.f, lB = 0.f, beforeA = 0.f, beforeB = 0.f;
+      bool guessed = false;
+      for (int next = s.k0; next < s.k1;) {
+        ok = warp_wait(sfull_bar, sp & 1, 51);
         if (!ok) break;
+        ++sp;
         tc_fence_after();
+        // Tiles in the middle of a segment are weighted with the running maximum as it
+        // stands; where one turns out to exceed it by more than 2^8 the MMA warp asks for the
+        // tile again (S is still there), which then goes through the exchange of maxima as a
+        // segment's first and last tiles do.
+        const bool redo = guessed && *s_over == tiles;
+        const int k = redo ? next - 1 : next;
+        const bool exchange = redo || k == s.k0 || k + 1 == s.k1;
+        if (redo) {
+          lA = beforeA;
+          lB = beforeB;
+        } else {
+          ++tiles;
+        }
         const uint32_t bad = *s_bad;
         uint32_t r[32];
         tmem_ld16x256b_x8(tmem + lane_addr + kTmemS + 64 * half, r);
         tmem_ld_wait();
         const int key0 = kKeys * k + 64 * half + 2 * c4;
-        float tA = -INFINITY, tB = -INFINITY;
-        if (bad == 0 && __all_sync(0xFFFFFFFFu, kKeys * (k + 1) <= min(seenA, seenB))) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              r[4 * j + e] = __float_as_uint(__uint_as_float(r[4 * j + e]) * scale_log2);
-              r[4 * j + 2 + e] = __float_as_uint(__uint_as_float(r[4 * j + 2 + e]) * scale_log2);
-              tA = fmaxf(tA, __uint_as_float(r[4 * j + e]));
-              tB = fmaxf(tB, __uint_as_float(r[4 * j + 2 + e]));
-            }
-        } else {
+        const bool whole = bad == 0 && __all_sync(0xFFFFFFFFu, kKeys * (k + 1) <= min(seenA, seenB));
+        if (!whole) {
 #pragma unroll
           for (int j = 0; j < 8; ++j)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const int key = key0 + 8 * j + e;
               const bool there = !((bad >> (4 * half + (j >> 1))) & 1u);
-              const float zA = there && key < seenA ? __uint_as_float(r[4 * j + e]) * scale_log2 : -INFINITY;
-              const float zB = there && key < seenB ? __uint_as_float(r[4 * j + 2 + e]) * scale_log2 : -INFINITY;
-              r[4 * j + e] = __float_as_uint(zA);
-              r[4 * j + 2 + e] = __float_as_uint(zB);
-              tA = fmaxf(tA, zA);
-              tB = fmaxf(tB, zB);
+              if (!there || key >= seenA) r[4 * j + e] = kMinusInf;
+              if (!there || key >= seenB) r[4 * j + 2 + e] = kMinusInf;
             }
         }
-#pragma unroll
-        for (int o = 1; o < 4; o <<= 1) {
-          tA = fmaxf(tA, __shfl_xor_sync(0xFFFFFFFFu, tA, o));
-          tB = fmaxf(tB, __shfl_xor_sync(0xFFFFFFFFu, tB, o));
-        }
-        // The running maximum moves only when a row sees its first key (its O and l are still
-        // zero) or when a tile exceeds it by more than 2^8: O is rescaled rarely, and weights
-        // up to 2^8 lose nothing in f32 or bf16.
-        const bool over = (mA != -INFINITY && tA > mA + kRescaleLog2) || (mB != -INFINITY && tB > mB + kRescaleLog2);
-        const bool vote = __any_sync(0xFFFFFFFFu, over);
-        if (c4 == 0) {
-          s_max[64 * half + rA] = tA;
-          s_max[64 * half + rB] = tB;
-        }
-        if (lane == 0) s_vote[warp - kSoftmaxWarp0] = vote ? 1u : 0u;
-        ok = group_sync(52);
-        if (!ok) break;
-        tA = fmaxf(tA, s_max[64 * (half ^ 1) + rA]);
-        tB = fmaxf(tB, s_max[64 * (half ^ 1) + rB]);
-        uint32_t any = 0;
-#pragma unroll
-        for (int w = 0; w < 8; ++w) any |= s_vote[w];
-        auto update = [](float& m, float& l, float t) {
-          float a = 1.f;
-          if (m == -INFINITY) {
-            m = t;
-          } else if (t > m + kRescaleLog2) {
-            a = exp2f(m - t);
-            m = t;
-            l *= a;
-          }
-          return a;
-        };
-        const float aA = update(mA, lA, tA), aB = update(mB, lB, tB);
-        if (any) {
-          // O^T: a thread's lane is a value dim, its columns the rows; each half takes two of
-          // the four blocks.  (S was issued behind the PV of the tile before, so that is done.)
-          if (half == 0 && c4 == 0) {
-            s_alpha[rA] = aA;
-            s_alpha[rB] = aB;
-          }
-          ok = group_sync(53);
-          if (!ok) break;
-#pragma unroll 1
-          for (int mb = 2 * half; mb < 2 * half + 2; ++mb)
-#pragma unroll 1
-            for (int c0 = 0; c0 < 64; c0 += 32) {
-              uint32_t o[32];
-              const uint32_t ta = tmem + lane_addr + kTmemO + 64 * mb + c0;
-              tmem_ld32(ta, o);
-              tmem_ld_wait();
-#pragma unroll
-              for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * s_alpha[c0 + c]);
-              tmem_st32(ta, o);
-            }
-          tmem_st_wait();
-        }
-        const float muA = mA == -INFINITY ? 0.f : mA, muB = mB == -INFINITY ? 0.f : mB;
+        float tA = -INFINITY, tB = -INFINITY;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float pA0 = exp2f(__uint_as_float(r[4 * j]) - muA), pA1 = exp2f(__uint_as_float(r[4 * j + 1]) - muA);
-          const float pB0 = exp2f(__uint_as_float(r[4 * j + 2]) - muB), pB1 = exp2f(__uint_as_float(r[4 * j + 3]) - muB);
-          lA += pA0 + pA1;
-          lB += pB0 + pB1;
-          // 16-byte chunk j of row r sits at chunk j ^ (r % 8) (128-byte swizzle)
-          *reinterpret_cast<uint32_t*>(prowA + ((j ^ (rA & 7)) << 4)) = pack_bf16x2(pA0, pA1);
-          *reinterpret_cast<uint32_t*>(prowB + ((j ^ (rB & 7)) << 4)) = pack_bf16x2(pB0, pB1);
+          tA = fmaxf(tA, fmaxf(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1])));
+          tB = fmaxf(tB, fmaxf(__uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3])));
         }
+        if (tA != -INFINITY) tA *= scale_log2;
+        if (tB != -INFINITY) tB *= scale_log2;
+        // The running maximum moves only when a row sees its first key or when a tile exceeds
+        // it by more than 2^8: O is rescaled rarely, and weights up to 2^8 lose nothing in f32
+        // or bf16.
+        if (!exchange) {
+          const bool over = (mA == -INFINITY ? tA != -INFINITY : tA > mA + kRescaleLog2) ||
+                            (mB == -INFINITY ? tB != -INFINITY : tB > mB + kRescaleLog2);
+          if (__any_sync(0xFFFFFFFFu, over) && lane == 0) *s_over = tiles;
+        } else {
+#pragma unroll
+          for (int o = 1; o < 4; o <<= 1) {
+            tA = fmaxf(tA, __shfl_xor_sync(0xFFFFFFFFu, tA, o));
+            tB = fmaxf(tB, __shfl_xor_sync(0xFFFFFFFFu, tB, o));
+          }
+          if (c4 == 0) {
+            s_max[64 * half + rA] = tA;
+            s_max[64 * half + rB] = tB;
+          }
+          ok = group_sync(52);
+          if (!ok) break;
+          tA = fmaxf(tA, s_max[64 * (half ^ 1) + rA]);
+          tB = fmaxf(tB, s_max[64 * (half ^ 1) + rB]);
+          auto update = [](float& m, float& l, float t) {
+            float a = 1.f;
+            if (m == -INFINITY) {
+              m = t;
+            } else if (t > m + kRescaleLog2) {
+              a = exp2_approx(m - t);
+              m = t;
+              l *= a;
+            }
+            return a;
+          };
+          const float aA = update(mA, lA, tA), aB = update(mB, lB, tB);
+          if (k > s.k0) {
+            const bool scaled = __any_sync(0xFFFFFFFFu, aA != 1.f || aB != 1.f);
+            if (half == 0) {
+              if (c4 == 0) {
+                s_alpha[rA] = aA;
+                s_alpha[rB] = aB;
+              }
+              if (lane == 0) s_vote[quarter] = scaled ? 1u : 0u;
+            }
+            ok = group_sync(53);
+            if (!ok) break;
+            if (s_vote[0] | s_vote[1] | s_vote[2] | s_vote[3]) {
+              // O^T: a thread's lane is a value dim, its columns the rows; each half takes two
+              // of the four blocks.  (S was issued behind the PV of the tile before, which is
+              // done.)
+#pragma unroll 1
+              for (int mb = 2 * half; mb < 2 * half + 2; ++mb)
+#pragma unroll 1
+                for (int c0 = 0; c0 < 64; c0 += 32) {
+                  uint32_t o[32];
+                  const uint32_t ta = tmem + lane_addr + kTmemO + 64 * mb + c0;
+                  tmem_ld32(ta, o);
+                  tmem_ld_wait();
+#pragma unroll
+                  for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * s_alpha[c0 + c]);
+                  tmem_st32(ta, o);
+                }
+              tmem_st_wait();
+            }
+          }
+        }
+        beforeA = lA;
+        beforeB = lB;
+        const float muA = mA == -INFINITY ? 0.f : mA, muB = mB == -INFINITY ? 0.f : mB;
+        float sumA0 = 0.f, sumA1 = 0.f, sumB0 = 0.f, sumB1 = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          float pA0 = exp2_approx(fmaf(__uint_as_float(r[4 * j]), scale_log2, -muA));
+          float pA1 = exp2_approx(fmaf(__uint_as_float(r[4 * j + 1]), scale_log2, -muA));
+          float pB0 = exp2_approx(fmaf(__uint_as_float(r[4 * j + 2]), scale_log2, -muB));
+          float pB1 = exp2_approx(fmaf(__uint_as_float(r[4 * j + 3]), scale_log2, -muB));
+          if (!whole) {  // a masked key weighs nothing, whatever the scale
+            if (r[4 * j] == kMinusInf) pA0 = 0.f;
+            if (r[4 * j + 1] == kMinusInf) pA1 = 0.f;
+            if (r[4 * j + 2] == kMinusInf) pB0 = 0.f;
+            if (r[4 * j + 3] == kMinusInf) pB1 = 0.f;
+          }
+          sumA0 += pA0;
+          sumA1 += pA1;
+          sumB0 += pB0;
+          sumB1 += pB1;
+          // 16-byte chunk j of row r sits at chunk j ^ (r % 8) (128-byte swizzle)
+          st_shared_u32(prowA + ((j ^ (rA & 7)) << 4), pack_bf16x2(pA0, pA1));
+          st_shared_u32(prowB + ((j ^ (rB & 7)) << 4), pack_bf16x2(pB0, pB1));
+        }
+        lA += sumA0 + sumA1;
+        lB += sumB0 + sumB1;
         if (bad != 0 || kKeys * (k + 1) > s.limit) {
           // rows that are no cached rows may hold anything, NaN included: as values they are zero
           for (int x = st; x < kKeys * 64; x += kSoftmaxThreads) {  // (row, 16-byte chunk of 8 blocks)
@@ -560,7 +652,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
         }
         fence_proxy_async();  // P (and the zeros) are visible to the tensor core
         tc_fence_before();
-        mbar_arrive(pfull_bar);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(pfull_bar);
+        guessed = !exchange;
+        next = k + 1;
       }
       if (!ok) break;
 #pragma unroll
@@ -610,7 +705,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
           }
         }
       tc_fence_before();
-      mbar_arrive(ofree_bar);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ofree_bar);
       ok = group_sync(56);  // s_l and s_m are free again
     }
   }
@@ -623,53 +719,80 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
   }
 }
 
-// Joins the parts of the query tiles that cross a border between shares:
+// Joins the parts of a query tile that crosses borders between shares:
 //   out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i,  M = max m_i.
-// Block (x, g): rows 8x .. 8x + 7 (one a warp) of the tile that CTA g is the first to
-// continue.  Its parts are CTA g - 1's last and the first of CTAs g, g + 1, ...
-__global__ void __launch_bounds__(256) paged_combine_kernel(PagedBatch p, int H, int ctas, const Share* shares,
-                                                            const float* parts, const float2* part_ml, uint16_t* out,
-                                                            float* lse) {
+// The parts are CTA g's last and the first of the CTAs behind it.  Four warps take a row, 128
+// value dims each, with eight parts' loads in flight beside those of their (m, l); the (tile,
+// row) pairs of all joins are spread over the whole grid, since a few long contexts leave few
+// tiles of many parts, and many short ones the other way round.
+constexpr int kJoinThreads = 256, kJoinRows = kJoinThreads / 128, kJoinBlocks = 3;  // blocks per SM
+__global__ void __launch_bounds__(kJoinThreads, kJoinBlocks)
+paged_combine_kernel(int ctas, const Join* joins, const float* parts, const float2* part_ml, uint16_t* out, float* lse) {
+  __shared__ int s_warp[kJoinThreads / 32];
+  __shared__ int4 s_join[kMaxCtas];  // CTAs that leave a tile to the next ones: (row0, nrows, parts, g)
+  static_assert(kMaxCtas <= kJoinThreads, "a thread a CTA");
   grid_dep_wait();
-  const int g = blockIdx.y + 1;
-  const Share s = load_share(shares + g);
-  if (s.b < 0 || s.k0 == 0) return;
-  const Share last = load_share(shares + g - 1);
-  if (last.b == s.b && last.tile == s.tile && last.k0 > 0) return;  // an earlier block's tile
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = 8 * blockIdx.x + warp;
-  const SequenceWork w = sequence_work(p, s.b, H);
-  if (kRows * s.tile + row >= w.rows) return;
-  int end = g + 1;  // CTAs g .. end - 1 continue the tile
-  for (; end < ctas; ++end) {
-    const Share t = load_share(shares + end);
-    if (t.b != s.b || t.tile != s.tile || t.k0 == 0) break;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int4 jv = make_int4(0, 0, 0, 0);
+  if ((int)threadIdx.x < ctas) jv = __ldcg(reinterpret_cast<const int4*>(joins + threadIdx.x));
+  const uint32_t votes = __ballot_sync(0xFFFFFFFFu, jv.z > 0);
+  if (lane == 0) s_warp[warp] = __popc(votes);
+  __syncthreads();
+  int count = 0, place = __popc(votes & ((1u << lane) - 1));
+  for (int i = 0; i < kJoinThreads / 32; ++i) {
+    place += i < warp ? s_warp[i] : 0;
+    count += s_warp[i];
   }
-  auto slot = [&](int i) { return i == g - 1 ? 2 * i + 1 : 2 * i; };
-  float M = -INFINITY;
-  for (int i = g - 1 + lane; i < end; i += 32) M = fmaxf(M, __ldcg(part_ml + (size_t)slot(i) * kRows + row).x);
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
-  float den = 0.f;
-  float4 acc[4];
-  for (int j = 0; j < 4; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i = g - 1; i < end; ++i) {
-    const float2 ml = __ldcg(part_ml + (size_t)slot(i) * kRows + row);
-    const float c = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
-    den += c * ml.y;
-    const float4* src = reinterpret_cast<const float4*>(parts + (size_t)slot(i) * kPartFloats + row * kDv) + lane;
-    for (int j = 0; j < 4; ++j) {
-      const float4 v = __ldcg(src + 32 * j);
-      acc[j].x += c * v.x;
-      acc[j].y += c * v.y;
-      acc[j].z += c * v.z;
-      acc[j].w += c * v.w;
+  if (jv.z > 0) s_join[place] = make_int4(jv.x, jv.y, jv.z, threadIdx.x);
+  __syncthreads();
+  const int d = 128 * (warp & 3) + 4 * lane;
+  for (int unit = kJoinRows * blockIdx.x + warp / 4; unit < count * kRows; unit += kJoinRows * gridDim.x) {
+    const int4 join = s_join[unit / kRows];
+    const int row = unit % kRows, n = join.z;
+    if (row >= join.y) continue;
+    auto slot = [&](int i) { return (size_t)(i == 0 ? 2 * join.w + 1 : 2 * (join.w + i)); };
+    float M = -INFINITY, den = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      const int m = min(32, n - i0);
+      float2 ml = make_float2(-INFINITY, 0.f);  // lane i holds part i0 + i's
+      if (lane < m) ml = __ldcg(part_ml + slot(i0 + lane) * kRows + row);
+      float c = 0.f;
+      for (int i = 0; i < m; i += 8) {
+        float4 v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (i + j < m) v[j] = __ldcg(reinterpret_cast<const float4*>(parts + slot(i0 + i + j) * kPartFloats + row * kDv + d));
+        if (i == 0) {  // the maximum so far, and the factors of these 32
+          float t = ml.x;
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, o));
+          const float big = fmaxf(M, t), old = M == -INFINITY ? 0.f : exp2_approx(M - big);
+          M = big;
+          c = ml.x == -INFINITY ? 0.f : exp2_approx(ml.x - M);
+          den = den * old + c * ml.y;
+          acc = make_float4(acc.x * old, acc.y * old, acc.z * old, acc.w * old);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float cj = __shfl_sync(0xFFFFFFFFu, c, (i + j) & 31);
+          if (i + j < m) {
+            acc.x += cj * v[j].x;
+            acc.y += cj * v[j].y;
+            acc.z += cj * v[j].z;
+            acc.w += cj * v[j].w;
+          }
+        }
+      }
     }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xFFFFFFFFu, den, o);
+    const float inv = den > 0.f ? 1.f / den : 0.f;
+    const size_t at = (size_t)join.x + row;
+    *reinterpret_cast<uint2*>(out + at * kDv + d) =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    if ((warp & 3) == 0 && lane == 0 && lse) lse[at] = den > 0.f ? (M + log2f(den)) * 0.69314718055994531f : -INFINITY;
   }
-  const float inv = den > 0.f ? 1.f / den : 0.f;
-  const size_t unit = (size_t)p.cu_q[s.b] * H + kRows * s.tile + row;
-  uint2* dst = reinterpret_cast<uint2*>(out + unit * kDv) + lane;
-  for (int j = 0; j < 4; ++j)
-    dst[32 * j] = make_uint2(pack_bf16x2(acc[j].x * inv, acc[j].y * inv), pack_bf16x2(acc[j].z * inv, acc[j].w * inv));
-  if (lane == 0 && lse) lse[unit] = den > 0.f ? (M + log2f(den)) * 0.69314718055994531f : -INFINITY;
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -683,15 +806,16 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// 2-D bf16 map over [rows][576] with a 64-column x box_rows box and 128-byte swizzle
-bool make_map_576(CUtensorMap* map, const void* base, long long rows, int box_rows) {
+// bf16 map over [rows][576] as [blocks of 64 columns][rows][64]: a box of box_rows rows and
+// box_blocks column blocks lands block after block, with the 128-byte swizzle
+bool make_map_576(CUtensorMap* map, const void* base, long long rows, int box_rows, int box_blocks) {
   auto fn = encode_fn();
   if (!fn) return false;
-  cuuint64_t dims[2] = {(cuuint64_t)kDqk, (cuuint64_t)rows};
-  cuuint64_t strides[1] = {(cuuint64_t)kDqk * 2};
-  cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
-  cuuint32_t estr[2] = {1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+  cuuint64_t dims[3] = {64, (cuuint64_t)rows, (cuuint64_t)kBlocks};
+  cuuint64_t strides[2] = {(cuuint64_t)kDqk * 2, 128};
+  cuuint32_t box[3] = {64, (cuuint32_t)box_rows, (cuuint32_t)box_blocks};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -699,15 +823,13 @@ bool make_map_576(CUtensorMap* map, const void* base, long long rows, int box_ro
 SymbolAddress g_err_addr;
 
 struct PagedLayout {
-  size_t before, plan, shares, part_ml, parts, total;
+  size_t joins, part_ml, parts, total;
 };
-size_t round256(size_t b) { return (b + 255) & ~(size_t)255; }
-PagedLayout paged_layout(int B, int ctas) {
+PagedLayout paged_layout(int ctas) {
+  auto round256 = [](size_t b) { return (b + 255) & ~(size_t)255; };
   PagedLayout l;
-  l.before = 0;
-  l.plan = round256((size_t)B * sizeof(long long));
-  l.shares = l.plan + 256;
-  l.part_ml = l.shares + round256((size_t)ctas * sizeof(Share));
+  l.joins = 0;
+  l.part_ml = round256((size_t)ctas * sizeof(Join));
   l.parts = l.part_ml + round256((size_t)ctas * 2 * kRows * sizeof(float2));
   l.total = l.parts + (size_t)ctas * 2 * kPartFloats * sizeof(float);
   return l;
@@ -715,14 +837,14 @@ PagedLayout paged_layout(int B, int ctas) {
 
 }  // namespace
 
-size_t paged_attn_workspace_bytes(long long, int B, int) {
-  const int sms = device_sm_count();
-  return sms > 0 ? paged_layout(B, sms).total : 0;
+size_t paged_attn_workspace_bytes() {
+  const int ctas = min(device_sm_count(), kMaxCtas);
+  return ctas > 0 ? paged_layout(ctas).total : 0;
 }
 
 cudaError_t launch_paged_attn(const uint16_t* q, const uint16_t* cache, const PagedBatch& p, int H, float scale,
                               uint16_t* out, float* lse, void* workspace, cudaStream_t stream) {
-  const int ctas = device_sm_count();
+  const int ctas = min(device_sm_count(), kMaxCtas);
   if (ctas <= 0) return cudaErrorInvalidDevice;
   static DeviceOnce once;
   cudaError_t e = once.run([] {
@@ -733,38 +855,29 @@ cudaError_t launch_paged_attn(const uint16_t* q, const uint16_t* cache, const Pa
   if ((e = g_err_addr.get(g_paged_error, &err)) != cudaSuccess) return e;
   int box = 16;  // rows of one copy: the largest power of two up to a tile that divides a page
   while (box < kKeys && p.page_size % (2 * box) == 0) box *= 2;
-  CUtensorMap qmap, cmap;
-  if (!make_map_576(&qmap, q, (long long)p.n * H, kRows) ||
-      !make_map_576(&cmap, cache, (long long)p.num_pages * p.page_size, box))
+  CUtensorMap qmap, cmap, rmap;
+  const long long pool = (long long)p.num_pages * p.page_size;
+  if (!make_map_576(&qmap, q, (long long)p.n * H, kRows, kBlocks) || !make_map_576(&cmap, cache, pool, box, 2) ||
+      !make_map_576(&rmap, cache, pool, box, 1))
     return cudaErrorInvalidValue;
-  const PagedLayout l = paged_layout(p.B, ctas);
+  const PagedLayout l = paged_layout(ctas);
   unsigned char* ws = static_cast<unsigned char*>(workspace);
-  Plan* plan = reinterpret_cast<Plan*>(ws + l.plan);
-  Share* shares = reinterpret_cast<Share*>(ws + l.shares);
+  Join* joins = reinterpret_cast<Join*>(ws + l.joins);
   float2* part_ml = reinterpret_cast<float2*>(ws + l.part_ml);
   float* parts = reinterpret_cast<float*>(ws + l.parts);
-  paged_plan_kernel<<<1, 1024, 0, stream>>>(p, H, ctas, reinterpret_cast<long long*>(ws + l.before), plan, shares);
+  paged_attn_kernel<<<ctas, kThreadsP, kSmemP, stream>>>(qmap, cmap, rmap, p, H, box, fabsf(scale) * 1.4426950408889634f,
+                                                         scale < 0.f ? 1u << 13 : 0u, cache, out, lse, joins, parts, part_ml, err);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // waits in-kernel
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(kThreadsP);
-  cfg.dynamicSmemBytes = kSmemP;
+  cfg.gridDim = dim3(kJoinBlocks * ctas);
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, paged_attn_kernel, qmap, cmap, p, H, box, scale * 1.4426950408889634f,
-                         static_cast<const Plan*>(plan), static_cast<const Share*>(shares), out, lse, parts, part_ml, err);
-  if (e != cudaSuccess || ctas == 1) return e;
-  cudaLaunchConfig_t ccfg = {};
-  ccfg.gridDim = dim3(kRows / 8, ctas - 1);
-  ccfg.blockDim = dim3(256);
-  ccfg.stream = stream;
-  ccfg.attrs = attr;
-  ccfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&ccfg, paged_combine_kernel, p, H, ctas, static_cast<const Share*>(shares),
+  return cudaLaunchKernelEx(&cfg, paged_combine_kernel, ctas, static_cast<const Join*>(joins),
                             static_cast<const float*>(parts), static_cast<const float2*>(part_ml), out, lse);
 }
 
