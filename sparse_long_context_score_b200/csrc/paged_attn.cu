@@ -14,13 +14,13 @@
 // CTAs' order (no atomics: the result does not depend on timing).
 //
 // One key tile of a CTA, everything in shared memory beside the 64 query rows (73.7 KB):
-//   S   = Q K^T    M = 64 rows, N = 128 keys, K = 576   (36 MMAs; TMEM lane = query row)
-//   O^T += V^T P^T M = 4 x 128 value dims, N = 64 rows, K = 128 keys (32 MMAs)
+//   S^T = K Q^T     M = 128 keys, N = 64 rows, K = 576        (36 MMAs; TMEM lane = key)
+//   O^T += V^T P^T  M = 4 x 128 value dims, N = 64 rows, K = 128 keys (32 MMAs)
 // The tile (147.5 KB) fills the rest of shared memory as nine blocks of 64 columns, and
 // there is no second one: S takes the blocks as they arrive, and each quarter of PV gives
-// two of them back, so the next tile's loads run behind PV and the next S behind the
-// loads.  (Two half tiles of 64 keys in turn would hide the softmax, but an MMA with M = 64
-// costs nearly as much at N = 64 as at N = 128: S would take 1.7 times as long.)
+// two of them back, so the next tile's loads run behind PV and the next S behind the loads.
+// Keys on the M side: an MMA of M = 128, N = 64, K = 16 takes 48 cycles (its operands'
+// 6 KB at 128 bytes a cycle); with the rows there, M = 64, N = 128 takes 64.
 #include <cudaTypedefs.h>
 
 #include "dsa_common.cuh"
@@ -80,11 +80,11 @@ struct Join {
 
 constexpr int kOffQ = 0;
 constexpr int kOffStage = kOffQ + kQBytes;
-constexpr int kOffMax = kOffStage + kStageBytes;     // [2][64] f32: a tile's maxima, per half of the keys
-constexpr int kOffAlpha = kOffMax + 2 * 64 * 4;      // [64] f32
-constexpr int kOffL = kOffAlpha + 64 * 4;            // [2][64] f32
-constexpr int kOffM = kOffL + 2 * 64 * 4;            // [64] f32
-constexpr int kOffVote = kOffM + 64 * 4;             // [4] u32: a lane quarter has a row to rescale
+constexpr int kOffMax = kOffStage + kStageBytes;     // [4][64] f32: a tile's maxima, per quarter of the keys
+constexpr int kOffAlpha = kOffMax + 4 * 64 * 4;      // [64] f32
+constexpr int kOffL = kOffAlpha + 64 * 4;            // [4][64] f32: a segment's sums, likewise
+constexpr int kOffM = kOffL + 4 * 64 * 4;            // [64] f32
+constexpr int kOffVote = kOffM + 64 * 4;             // [2] u32: a half of the rows has one to rescale
 constexpr int kOffOver = kOffVote + 16;              // u32: number of the last guessed tile that exceeded the maximum
 constexpr int kOffBad = kOffOver + 16;               // u32: 16-row groups of the tile that are not there
 constexpr int kOffShare = kOffBad + 16;
@@ -98,12 +98,12 @@ static_assert(kOffBar % 8 == 0, "barrier alignment");
 static_assert(kSmemP <= 232448, "shared memory budget");
 
 constexpr int kTmemO = 0;      // O^T: 4 blocks x 64 columns, all 128 lanes
-constexpr int kTmemS = 256;    // S: 128 columns, lanes 0..15 of each quarter
+constexpr int kTmemS = 256;    // S^T: 64 columns, all 128 lanes
 constexpr int kTmemCols = 512;
 
 constexpr int kPartFloats = kRows * kDv;             // one part's [64][512] sums
 
-constexpr uint32_t kMinusInf = 0xFF800000u;
+constexpr float kRescaleFactor = 256.f;  // 2^kRescaleLog2
 
 // 2^x; results below the normal range become zero
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -112,8 +112,22 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
-__device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t v) {
-  asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float min_nan(float x, float y) {  // NaN if x is
+  float z;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(x), "f"(y));
+  return z;
+}
+// natural logarithm of 2^m sum; -inf for an empty sum
+__device__ __forceinline__ float log_sum(float m, float sum) {
+  return sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.69314718055994531f;
+}
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
 // Query rows of a sequence and the cached rows that they see.
@@ -413,13 +427,13 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------------ tensor core
     const bool leader = elect_one();
-    // Q (K-major) x K (K-major); a negative scale negates Q, so that the largest S is the
+    // K (K-major) x Q (K-major); a negative scale negates K, so that the largest S is the
     // largest logit
-    const uint32_t idS = idesc_bf16_f32(kRows, kKeys) | negate;
-    constexpr uint32_t idPV = idesc_bf16_f32(128, kRows, true, false);  // V^T (M-major) x P (K-major)
+    const uint32_t idS = idesc_bf16_f32(kKeys, kRows) | negate;
+    constexpr uint32_t idPV = idesc_bf16_f32(128, kRows, true, true);  // V^T (M-major) x P (N-major)
     const uint64_t dq = sdesc_kmajor_sw128(sQ), dk = sdesc_kmajor_sw128(sStage);
     const uint64_t dv = sdesc_mnmajor_sw128(sStage, kBlockBytes, 1024);
-    const uint64_t dp = sdesc_kmajor_sw128(sStage + kPBlock * kBlockBytes);
+    const uint64_t dp = sdesc_mnmajor_sw128(sStage + kPBlock * kBlockBytes, 1024, 1024);
     Segment s;
     int it = 0;
     uint32_t pp = 0;  // phases of pfull seen
@@ -436,8 +450,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
           if (leader) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              mma_bf16(tmem + kTmemS, dq + (uint64_t)((kb * kQBlockBytes + kk * 32) >> 4),
-                       dk + (uint64_t)((kb * kBlockBytes + kk * 32) >> 4), idS, kb + kk > 0);
+              mma_bf16(tmem + kTmemS, dk + (uint64_t)((kb * kBlockBytes + kk * 32) >> 4),
+                       dq + (uint64_t)((kb * kQBlockBytes + kk * 32) >> 4), idS, kb + kk > 0);
           }
           __syncwarp();
         }
@@ -465,7 +479,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
 #pragma unroll
             for (int ks = 0; ks < kKeys / 16; ++ks)
               mma_bf16(tmem + kTmemO + 64 * mb, dv + (uint64_t)((2 * mb * kBlockBytes + ks * 16 * 128) >> 4),
-                       dp + (uint64_t)(((ks >> 2) * (kBlockBytes / 2) + (ks & 3) * 32) >> 4), idPV,
+                       dp + (uint64_t)(ks * 16 * 128 >> 4), idPV,
                        k > s.k0 || ks > 0 ? 1u : 0u);
             mma_commit(free_bar(mb));
           }
@@ -482,15 +496,15 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
     __syncwarp();
   } else {
     // ------------------------------------------------------------------ softmax and epilogue
-    // Warp w reads TMEM lane quarter w % 4 and keys [64 half, 64 half + 64) of a tile: a
-    // thread gets rows rA = 16 quarter + lane / 4 and rB = rA + 8, keys 8 j + 2 (lane % 4) +
-    // {0, 1} of the half (j < 8).
-    const int quarter = warp & 3, half = (warp - kSoftmaxWarp0) >> 2, c4 = lane & 3;
-    const int rA = 16 * quarter + (lane >> 2), rB = rA + 8;
+    // Warp w reads TMEM lane quarter w % 4, i.e. keys 32 quarter .. 32 quarter + 31 of a tile,
+    // a lane a key, and 32 of the 64 rows.  A row's running maximum is the same in all of its
+    // threads, and each keeps its own key's share of the row's sum to the end of a segment:
+    // no tile needs a reduction over keys.
+    const int quarter = warp & 3, half = (warp - kSoftmaxWarp0) >> 2;
     const uint32_t lane_addr = (uint32_t)(32 * quarter) << 16;
     const int st = threadIdx.x - 32 * kSoftmaxWarp0;  // 0 .. 255
-    const uint32_t pbase = sStage + kPBlock * kBlockBytes + half * (kBlockBytes / 2);
-    const uint32_t prowA = pbase + rA * 128 + 4 * c4, prowB = pbase + rB * 128 + 4 * c4;
+    // P: a row of 128 bytes a key, 64 query rows; 16-byte chunk c of key x at chunk c ^ (x % 8)
+    const uint32_t prow = sStage + kPBlock * kBlockBytes + (32 * quarter + lane) * 128;
     uint32_t grp_phase = 0;
     auto group_sync = [&](int code) {
       __syncwarp();
@@ -500,14 +514,18 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
       return ok;
     };
     Segment s;
-    uint32_t sp = 0;    // phases of sfull seen
+    uint32_t sp = 0;     // phases of sfull seen
     uint32_t tiles = 0;  // key tiles weighted, this CTA's first being number 1
     bool ok = true;
     for (int i = 0; ok && next_segment(s); ++i) {
-      // cached rows that this thread's query rows see
-      const int seenA = rA < s.nrows ? max(0, min(s.seen0 + (s.tile_row + rA) / H, s.limit)) : 0;
-      const int seenB = rB < s.nrows ? max(0, min(s.seen0 + (s.tile_row + rB) / H, s.limit)) : 0;
-      float mA = -INFINITY, mB = -INFINITY, lA = 0.f, lB = 0.f, beforeA = 0.f, beforeB = 0.f;
+      const int seen_first = min(s.seen0 + s.tile_row / H, s.limit);  // rows that all 64 see
+      float m[32], l[32];
+      float mrow = 32 * half + lane < s.nrows ? -INFINITY : INFINITY;  // row 32 half + lane's maximum
+#pragma unroll
+      for (int r = 0; r < 32; ++r) {
+        m[r] = 32 * half + r < s.nrows ? -INFINITY : INFINITY;  // (a row that is none weighs nothing)
+        l[r] = 0.f;
+      }
       bool guessed = false;
       for (int next = s.k0; next < s.k1;) {
         ok = warp_wait(sfull_bar, sp & 1, 51);
@@ -521,82 +539,68 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
         const bool redo = guessed && *s_over == tiles;
         const int k = redo ? next - 1 : next;
         const bool exchange = redo || k == s.k0 || k + 1 == s.k1;
-        if (redo) {
-          lA = beforeA;
-          lB = beforeB;
-        } else {
-          ++tiles;
-        }
+        if (!redo) ++tiles;
         const uint32_t bad = *s_bad;
-        uint32_t r[32];
-        tmem_ld16x256b_x8(tmem + lane_addr + kTmemS + 64 * half, r);
-        tmem_ld_wait();
-        const int key0 = kKeys * k + 64 * half + 2 * c4;
-        const bool whole = bad == 0 && __all_sync(0xFFFFFFFFu, kKeys * (k + 1) <= min(seenA, seenB));
+        uint32_t z[32];
+        tmem_ld32(tmem + lane_addr + kTmemS + 32 * half, z);
+        // rows from `from` on (of this warp's 32) see this thread's key
+        const int key = kKeys * k + 32 * quarter + lane;
+        const bool whole = bad == 0 && kKeys * (k + 1) <= seen_first;
+        int from = 0;
         if (!whole) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int key = key0 + 8 * j + e;
-              const bool there = !((bad >> (4 * half + (j >> 1))) & 1u);
-              if (!there || key >= seenA) r[4 * j + e] = kMinusInf;
-              if (!there || key >= seenB) r[4 * j + 2 + e] = kMinusInf;
-            }
+          const bool there = key < s.limit && !((bad >> (2 * quarter + (lane >> 4))) & 1u);
+          const long long first = (long long)(key + 1 - s.seen0) * H - s.tile_row - 32 * half;
+          from = there ? (int)max(0LL, min(32LL, first)) : 32;
         }
-        float tA = -INFINITY, tB = -INFINITY;
+        tmem_ld_wait();
+        // this thread's key for row r
+        auto weight = [&](int r) {
+          const float p = min_nan(exp2_approx(fmaf(__uint_as_float(z[r]), scale_log2, -m[r])), 2.f * kRescaleFactor);
+          return !whole && r < from ? 0.f : p;  // (a masked key weighs nothing whatever its logit and the scale)
+        };
+        // A guess is taken back by subtracting what it added: that costs the row's sum one
+        // rounding, since weights are capped (above the cap the guess is wrong anyway).
+        if (redo) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          tA = fmaxf(tA, fmaxf(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1])));
-          tB = fmaxf(tB, fmaxf(__uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3])));
+          for (int r = 0; r < 32; ++r) l[r] -= weight(r);
         }
-        if (tA != -INFINITY) tA *= scale_log2;
-        if (tB != -INFINITY) tB *= scale_log2;
         // The running maximum moves only when a row sees its first key or when a tile exceeds
         // it by more than 2^8: O is rescaled rarely, and weights up to 2^8 lose nothing in f32
         // or bf16.
-        if (!exchange) {
-          const bool over = (mA == -INFINITY ? tA != -INFINITY : tA > mA + kRescaleLog2) ||
-                            (mB == -INFINITY ? tB != -INFINITY : tB > mB + kRescaleLog2);
-          if (__any_sync(0xFFFFFFFFu, over) && lane == 0) *s_over = tiles;
-        } else {
+        if (exchange) {
+          float mine = -INFINITY;  // of row 32 half + lane over the warp's keys
 #pragma unroll
-          for (int o = 1; o < 4; o <<= 1) {
-            tA = fmaxf(tA, __shfl_xor_sync(0xFFFFFFFFu, tA, o));
-            tB = fmaxf(tB, __shfl_xor_sync(0xFFFFFFFFu, tB, o));
+          for (int r = 0; r < 32; ++r) {
+            const float t = warp_max(r >= from ? __uint_as_float(z[r]) * scale_log2 : -INFINITY);
+            if (lane == r) mine = t;
           }
-          if (c4 == 0) {
-            s_max[64 * half + rA] = tA;
-            s_max[64 * half + rB] = tB;
-          }
+          s_max[64 * quarter + 32 * half + lane] = mine;
           ok = group_sync(52);
           if (!ok) break;
-          tA = fmaxf(tA, s_max[64 * (half ^ 1) + rA]);
-          tB = fmaxf(tB, s_max[64 * (half ^ 1) + rB]);
-          auto update = [](float& m, float& l, float t) {
-            float a = 1.f;
-            if (m == -INFINITY) {
-              m = t;
-            } else if (t > m + kRescaleLog2) {
-              a = exp2_approx(m - t);
-              m = t;
-              l *= a;
-            }
-            return a;
-          };
-          const float aA = update(mA, lA, tA), aB = update(mB, lB, tB);
+          float t = -INFINITY;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) t = fmaxf(t, s_max[64 * q + 32 * half + lane]);
+          float alpha = 1.f;
+          if (mrow == -INFINITY) {
+            mrow = t;
+          } else if (t > mrow + kRescaleLog2) {
+            alpha = exp2_approx(mrow - t);
+            mrow = t;
+          }
+          const bool scaled = __any_sync(0xFFFFFFFFu, alpha != 1.f);
+#pragma unroll
+          for (int r = 0; r < 32; ++r) {
+            m[r] = __shfl_sync(0xFFFFFFFFu, mrow, r);
+            l[r] *= __shfl_sync(0xFFFFFFFFu, alpha, r);
+          }
           if (k > s.k0) {
-            const bool scaled = __any_sync(0xFFFFFFFFu, aA != 1.f || aB != 1.f);
-            if (half == 0) {
-              if (c4 == 0) {
-                s_alpha[rA] = aA;
-                s_alpha[rB] = aB;
-              }
-              if (lane == 0) s_vote[quarter] = scaled ? 1u : 0u;
+            if (quarter == 0) {
+              s_alpha[32 * half + lane] = alpha;
+              if (lane == 0) s_vote[half] = scaled ? 1u : 0u;
             }
             ok = group_sync(53);
             if (!ok) break;
-            if (s_vote[0] | s_vote[1] | s_vote[2] | s_vote[3]) {
+            if (s_vote[0] | s_vote[1]) {
               // O^T: a thread's lane is a value dim, its columns the rows; each half takes two
               // of the four blocks.  (S was issued behind the PV of the tile before, which is
               // done.)
@@ -616,32 +620,20 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
             }
           }
         }
-        beforeA = lA;
-        beforeB = lB;
-        const float muA = mA == -INFINITY ? 0.f : mA, muB = mB == -INFINITY ? 0.f : mB;
-        float sumA0 = 0.f, sumA1 = 0.f, sumB0 = 0.f, sumB1 = 0.f;
+        float most = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          float pA0 = exp2_approx(fmaf(__uint_as_float(r[4 * j]), scale_log2, -muA));
-          float pA1 = exp2_approx(fmaf(__uint_as_float(r[4 * j + 1]), scale_log2, -muA));
-          float pB0 = exp2_approx(fmaf(__uint_as_float(r[4 * j + 2]), scale_log2, -muB));
-          float pB1 = exp2_approx(fmaf(__uint_as_float(r[4 * j + 3]), scale_log2, -muB));
-          if (!whole) {  // a masked key weighs nothing, whatever the scale
-            if (r[4 * j] == kMinusInf) pA0 = 0.f;
-            if (r[4 * j + 1] == kMinusInf) pA1 = 0.f;
-            if (r[4 * j + 2] == kMinusInf) pB0 = 0.f;
-            if (r[4 * j + 3] == kMinusInf) pB1 = 0.f;
+        for (int r0 = 0; r0 < 32; r0 += 8) {
+          float p[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            p[j] = weight(r0 + j);
+            l[r0 + j] += p[j];
+            most = fmaxf(most, p[j]);
           }
-          sumA0 += pA0;
-          sumA1 += pA1;
-          sumB0 += pB0;
-          sumB1 += pB1;
-          // 16-byte chunk j of row r sits at chunk j ^ (r % 8) (128-byte swizzle)
-          st_shared_u32(prowA + ((j ^ (rA & 7)) << 4), pack_bf16x2(pA0, pA1));
-          st_shared_u32(prowB + ((j ^ (rB & 7)) << 4), pack_bf16x2(pB0, pB1));
+          st_shared_v4(prow + (((4 * half + r0 / 8) ^ (lane & 7)) << 4), pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3]),
+                       pack_bf16x2(p[4], p[5]), pack_bf16x2(p[6], p[7]));
         }
-        lA += sumA0 + sumA1;
-        lB += sumB0 + sumB1;
+        if (!exchange && __any_sync(0xFFFFFFFFu, most > kRescaleFactor) && lane == 0) *s_over = tiles;
         if (bad != 0 || kKeys * (k + 1) > s.limit) {
           // rows that are no cached rows may hold anything, NaN included: as values they are zero
           for (int x = st; x < kKeys * 64; x += kSoftmaxThreads) {  // (row, 16-byte chunk of 8 blocks)
@@ -658,29 +650,32 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
         next = k + 1;
       }
       if (!ok) break;
+      // sums over the warp's keys, row 32 half + lane to each lane: at step o the rows whose
+      // index has bit o go to the lanes that have it
 #pragma unroll
-      for (int o = 1; o < 4; o <<= 1) {
-        lA += __shfl_xor_sync(0xFFFFFFFFu, lA, o);
-        lB += __shfl_xor_sync(0xFFFFFFFFu, lB, o);
-      }
-      if (c4 == 0) {
-        s_l[64 * half + rA] = lA;
-        s_l[64 * half + rB] = lB;
-        if (half == 0) {
-          s_m[rA] = mA;
-          s_m[rB] = mB;
+      for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int r = 0; r < o; ++r) {
+          const float keep = lane & o ? l[r + o] : l[r], give = lane & o ? l[r] : l[r + o];
+          l[r] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, o);
         }
-      }
+      s_l[64 * quarter + 32 * half + lane] = l[0];
+      if (quarter == 0) s_m[32 * half + lane] = mrow;
       ok = group_sync(54) && warp_wait(ofull_bar, i & 1, 55);
       if (!ok) break;
       tc_fence_after();
-      if (st < s.nrows) {
-        const float m = s_m[st], l = s_l[st] + s_l[64 + st];
-        if (s.part >= 0)
-          part_ml[(size_t)s.part * kRows + st] = make_float2(m, l);
-        else if (lse)
-          lse[(size_t)s.row0 + st] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+      if (st < 64) {
+        const float sum = (s_l[st] + s_l[64 + st]) + (s_l[128 + st] + s_l[192 + st]);
+        if (st < s.nrows) {
+          if (s.part >= 0)
+            part_ml[(size_t)s.part * kRows + st] = make_float2(s_m[st], sum);
+          else if (lse)
+            lse[(size_t)s.row0 + st] = log_sum(s_m[st], sum);
+        }
+        s_alpha[st] = sum == 0.f ? 0.f : 1.f / sum;
       }
+      ok = group_sync(57);
+      if (!ok) break;
 #pragma unroll 1
       for (int mb = 2 * half; mb < 2 * half + 2; ++mb)
 #pragma unroll 1
@@ -698,16 +693,13 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
             uint16_t* dst = out + ((size_t)s.row0 + c0) * kDv + d;
 #pragma unroll
             for (int c = 0; c < 32; ++c)
-              if (c < rows) {
-                const float l = s_l[c0 + c] + s_l[64 + c0 + c];
-                dst[(size_t)c * kDv] = (uint16_t)pack_bf16x2(l > 0.f ? __uint_as_float(o[c]) / l : 0.f, 0.f);
-              }
+              if (c < rows) dst[(size_t)c * kDv] = (uint16_t)pack_bf16x2(__uint_as_float(o[c]) * s_alpha[c0 + c], 0.f);
           }
         }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(ofree_bar);
-      ok = group_sync(56);  // s_l and s_m are free again
+      ok = group_sync(56);  // s_l, s_m and s_alpha are free again
     }
   }
 
@@ -769,7 +761,7 @@ paged_combine_kernel(int ctas, const Join* joins, const float* parts, const floa
           for (int o = 16; o > 0; o >>= 1) t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, o));
           const float big = fmaxf(M, t), old = M == -INFINITY ? 0.f : exp2_approx(M - big);
           M = big;
-          c = ml.x == -INFINITY ? 0.f : exp2_approx(ml.x - M);
+          c = ml.y == 0.f ? 0.f : ml.x == -INFINITY ? ml.y : exp2_approx(ml.x - M);  // (a NaN sum stays one)
           den = den * old + c * ml.y;
           acc = make_float4(acc.x * old, acc.y * old, acc.z * old, acc.w * old);
         }
@@ -787,11 +779,11 @@ paged_combine_kernel(int ctas, const Join* joins, const float* parts, const floa
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xFFFFFFFFu, den, o);
-    const float inv = den > 0.f ? 1.f / den : 0.f;
+    const float inv = den == 0.f ? 0.f : 1.f / den;
     const size_t at = (size_t)join.x + row;
     *reinterpret_cast<uint2*>(out + at * kDv + d) =
         make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-    if ((warp & 3) == 0 && lane == 0 && lse) lse[at] = den > 0.f ? (M + log2f(den)) * 0.69314718055994531f : -INFINITY;
+    if ((warp & 3) == 0 && lane == 0 && lse) lse[at] = log_sum(M, den);
   }
 }
 
