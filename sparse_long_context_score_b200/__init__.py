@@ -443,30 +443,49 @@ def dsa_decode_step(groups, k: int, scale: float, ws=None, stream=None, side=Non
 
 
 # ---------------------------------------------------------------- around the verify step
-def _device(*tensors):
-    """The CUDA device that all the given tensors (None skipped) lie on."""
-    dev = None
-    for t in tensors:
-        if t is None:
-            continue
-        if not isinstance(t, _torch().Tensor):
-            raise TypeError(f"expected a torch.Tensor, got {type(t).__name__}")
-        if not t.is_cuda:
-            raise ValueError("expected CUDA tensors (there is no CPU path)")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}: all must be on one device")
-    return dev
+# These calls are short: a decode step's take a few microseconds on the GPU, so the checks
+# below are kept to one pass over each tensor.
+def _arg(t, dtypes, shape, name, dev):
+    """Address of a dense tensor on `dev` (None: a null pointer)."""
+    if t is None:
+        return None
+    if not isinstance(t, _torch().Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
-def _on(dev, call, stream):
-    """`call(raw stream)` with `dev` current; the default stream is dev's current one."""
+def _device(t, name):
+    """The CUDA device of a tensor."""
+    if not isinstance(t, _torch().Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
+    return t.device
+
+
+def _call(name, dev, stream, *args):
+    """The C call `name` with `dev` current, on `stream` (None: the current one of `dev`)."""
     torch = _torch()
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(dev.index)
+    else:
+        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    fn = getattr(lib(), name)
     if dev.index == torch.cuda.current_device():
-        return call(_stream(stream))
-    with torch.cuda.device(dev):
-        return call(_stream(stream))
+        rc = fn(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, raw)
+    if rc != DSA_OK:
+        _check(rc, name)
 
 
 def dsa_rope_init(rot_dim: int, layout: str = "interleaved", theta: float = 10000.0, factor: float = 1.0,
@@ -486,47 +505,51 @@ def dsa_rope(x, positions, plan: RopePlan, rot_offset: int = 0, out=None, stream
     positions [n] int64 -> out: entries [rot_offset, rot_offset + plan.rot_dim) of each head
     rotated, the others copied.  `out` may be x (in place) or a strided tensor apart from it."""
     torch = _torch()
+    dev = _device(x, "x")
     n, heads, dim = x.shape
     if out is None:
-        out = torch.empty((n, heads, dim), dtype=x.dtype, device=x.device)
-    dev = _device(x, positions, out)
-    if x.dtype not in (torch.bfloat16, torch.float32) or out.dtype != x.dtype:
-        raise TypeError(f"x and out must both be bf16 or both float32, got {x.dtype} and {out.dtype}")
-    if out.shape != x.shape or (dim > 1 and (x.stride(2) != 1 or out.stride(2) != 1)):
+        out = torch.empty((n, heads, dim), dtype=x.dtype, device=dev)
+    elif _device(out, "out") != dev:
+        raise ValueError(f"out is on {out.device}, expected {dev}")
+    dtype = x.dtype
+    if dtype not in (torch.bfloat16, torch.float32) or out.dtype != dtype:
+        raise TypeError(f"x and out must both be bf16 or both float32, got {dtype} and {out.dtype}")
+    xs, os_ = x.stride(), out.stride()
+    if out.shape != x.shape or (dim > 1 and (xs[2] != 1 or os_[2] != 1)):
         raise ValueError("out must have x's shape, and both a dense last dimension")
-    args = (x.data_ptr(), _ptr(positions, (torch.int64,), "positions", (n,)), n, heads, dim, int(rot_offset),
-            ctypes.addressof(plan), int(x.dtype == torch.float32), x.stride(0), x.stride(1), out.data_ptr(), out.stride(0),
-            out.stride(1))
+    ptr = _arg(positions, (torch.int64,), (n,), "positions", dev)
     if n and heads:
-        _check(_on(dev, lambda s: lib().dsa_rope(*args, s), stream), "dsa_rope")
+        _call("dsa_rope", dev, stream, x.data_ptr(), ptr, n, heads, dim, int(rot_offset), ctypes.addressof(plan),
+              int(dtype == torch.float32), xs[0], xs[1], out.data_ptr(), os_[0], os_[1])
     return out
 
 
-def _paged(n, cache, table, cu_q, ctx_len):
-    """Checked pointers and sizes of a paged batch, as the C calls take them."""
+def _paged(cache, table, cu_q, ctx_len, dev):
+    """Checked pointers of a paged batch, its sequences, and the pool's sizes."""
     torch = _torch()
+    i32 = (torch.int32,)
+    _device(cache, "cache"), _device(table, "table")
     if cache.dim() != 3 or table.dim() != 2:
         raise ValueError("cache must be [pages, page_size, 576] and table [B, max_pages]")
     P, page, _ = cache.shape
     B, most = table.shape
-    i32 = (torch.int32,)
-    return (_ptr(cache, _bf16_types(), "cache", (P, page, DQK)), _ptr(table, i32, "table"),
-            _ptr(cu_q, i32, "cu_q", (B + 1,)), _ptr(ctx_len, i32, "ctx_len", (B,))), (n, B), (P, page, most)
+    return (_arg(cache, _bf16_types(), (P, page, DQK), "cache", dev), _arg(table, i32, (B, most), "table", dev),
+            _arg(cu_q, i32, (B + 1,), "cu_q", dev), _arg(ctx_len, i32, (B,), "ctx_len", dev)), B, (P, page, most)
 
 
 def dsa_cache_append(x, gamma, eps: float, plan: RopePlan, cache, table, cu_q, ctx_len, stream=None):
     """Normalises, rotates and writes the new tokens' rows x [n, 576] bf16 (rows may be
     strided) to the pages of their sequences; gamma [512] bf16, cache [pages, page_size, 576]
     bf16, table [B, max_pages], cu_q [B+1] and ctx_len [B] int32.  Returns cache."""
-    dev = _device(x, gamma, cache, table, cu_q, ctx_len)
+    dev = _device(x, "x")
     if x.dtype not in _bf16_types() or x.dim() != 2 or x.shape[1] != DQK or x.stride(1) != 1:
         raise ValueError(f"x must be [n, {DQK}] bf16 with dense rows")
     n = x.shape[0]
-    ptrs, sizes, pages = _paged(n, cache, table, cu_q, ctx_len)
-    args = (x.data_ptr(), x.stride(0) if n > 1 else DQK, _ptr(gamma, _bf16_types(), "gamma", (DV,)), float(eps),
-            ctypes.addressof(plan), *ptrs, *sizes, *pages)
+    ptrs, B, pages = _paged(cache, table, cu_q, ctx_len, dev)
+    gm = _arg(gamma, _bf16_types(), (DV,), "gamma", dev)
     if n:
-        _check(_on(dev, lambda s: lib().dsa_cache_append(*args, s), stream), "dsa_cache_append")
+        _call("dsa_cache_append", dev, stream, x.data_ptr(), x.stride(0) if n > 1 else DQK, gm, float(eps),
+              ctypes.addressof(plan), *ptrs, n, B, *pages)
     return cache
 
 
@@ -545,20 +568,22 @@ def dsa_paged_attn(q, cache, table, cu_q, ctx_len, scale: float, out=None, lse=N
     """Attention of the new tokens q [n, H, 576] bf16 over their sequences' rows in a paged
     cache (see dsa_cache_append) -> (out [n, H, 512] bf16, lse [n, H] f32)."""
     torch = _torch()
+    dev = _device(q, "q")
     n, H, _ = q.shape
     if out is None:
-        out = torch.empty((n, H, DV), dtype=torch.bfloat16, device=q.device)
+        out = torch.empty((n, H, DV), dtype=torch.bfloat16, device=dev)
     if lse is None:
-        lse = torch.empty((n, H), dtype=torch.float32, device=q.device)
+        lse = torch.empty((n, H), dtype=torch.float32, device=dev)
+    ptrs, B, pages = _paged(cache, table, cu_q, ctx_len, dev)
     if ws is None:
-        ws = paged_workspace(n, table.shape[0], H, q.device)
-    dev = _device(q, cache, table, cu_q, ctx_len, out, lse, ws)
-    ptrs, sizes, pages = _paged(n, cache, table, cu_q, ctx_len)
-    args = (_ptr(q, _bf16_types(), "q", (n, H, DQK)), *ptrs, *sizes, H, *pages, float(scale),
-            _ptr(out, _bf16_types(), "out", (n, H, DV)), _ptr(lse, (torch.float32,), "lse", (n, H)),
+        ws = paged_workspace(n, B, H, dev)
+    args = (_arg(q, _bf16_types(), (n, H, DQK), "q", dev), *ptrs, n, B, H, *pages, float(scale),
+            _arg(out, _bf16_types(), (n, H, DV), "out", dev), _arg(lse, (torch.float32,), (n, H), "lse", dev),
             _ptr(ws, (torch.uint8,), "workspace"), ws.numel())
+    if ws.device != dev:
+        raise ValueError(f"workspace is on {ws.device}, expected {dev}")
     if n:
-        _check(_on(dev, lambda s: lib().dsa_paged_attn(*args, s), stream), "dsa_paged_attn")
+        _call("dsa_paged_attn", dev, stream, *args)
     return out, lse
 
 
@@ -571,12 +596,11 @@ def dsa_logits_probs(logits, temperature=None, history=None, history_len=None, p
     bias_values [B, nb]), an allow mask (mask [B, S, ceil(V/32)] int32 bits), and the softmax
     at temperature [B] (0: one-hot at the maximum)."""
     torch = _torch()
+    dev = _device(logits, "logits")
     B, S, V = logits.shape
     if out is None:
-        out = torch.empty((B, S, V), dtype=torch.float32, device=logits.device)
-    dev = _device(logits, temperature, history, history_len, prompt_len, draft, repetition, frequency, presence, bias_ids,
-                  bias_values, mask, out)
-    f32, i32 = (torch.float32,), (torch.int32,)
+        out = torch.empty((B, S, V), dtype=torch.float32, device=dev)
+    f32, i32, row = (torch.float32,), (torch.int32,), (B,)
     cap = nb = 0
     if history is not None:
         cap = history.shape[1]
@@ -586,13 +610,13 @@ def dsa_logits_probs(logits, temperature=None, history=None, history_len=None, p
         raise ValueError("bias_ids and bias_values go together")
     if bias_ids is not None:
         nb = bias_ids.shape[1]
-    args = (_ptr(logits, (torch.float32, torch.bfloat16), "logits"), int(logits.dtype == torch.float32), B, S, V,
-            _ptr(temperature, f32, "temperature", (B,)), _ptr(repetition, f32, "repetition", (B,)),
-            _ptr(frequency, f32, "frequency", (B,)), _ptr(presence, f32, "presence", (B,)),
-            _ptr(history, i32, "history", (B, cap)), cap, _ptr(history_len, i32, "history_len", (B,)),
-            _ptr(prompt_len, i32, "prompt_len", (B,)), _ptr(draft, i32, "draft", (B, S)),
-            _ptr(bias_ids, i32, "bias_ids", (B, nb)), _ptr(bias_values, f32, "bias_values", (B, nb)), nb,
-            _ptr(mask, i32, "mask", (B, S, (V + 31) // 32)), _ptr(out, f32, "out", (B, S, V)))
+    args = (_arg(logits, (torch.float32, torch.bfloat16), (B, S, V), "logits", dev), int(logits.dtype == torch.float32),
+            B, S, V, _arg(temperature, f32, row, "temperature", dev), _arg(repetition, f32, row, "repetition", dev),
+            _arg(frequency, f32, row, "frequency", dev), _arg(presence, f32, row, "presence", dev),
+            _arg(history, i32, (B, cap), "history", dev), cap, _arg(history_len, i32, row, "history_len", dev),
+            _arg(prompt_len, i32, row, "prompt_len", dev), _arg(draft, i32, (B, S), "draft", dev),
+            _arg(bias_ids, i32, (B, nb), "bias_ids", dev), _arg(bias_values, f32, (B, nb), "bias_values", dev), nb,
+            _arg(mask, i32, (B, S, (V + 31) // 32), "mask", dev), _arg(out, f32, (B, S, V), "out", dev))
     if B and S:
-        _check(_on(dev, lambda s: lib().dsa_logits_probs(*args, s), stream), "dsa_logits_probs")
+        _call("dsa_logits_probs", dev, stream, *args)
     return out
