@@ -469,18 +469,22 @@ dsa_status dsa_paged_attn(const uint16_t *q, const uint16_t *cache, const int32_
  *   temperature, repetition, frequency, presence  [B] f32  NULL: 1, 1, 0, 0
  *   history      [B, history_cap] i32   NULL: none; its first history_len[b] entries count
  *                                       (NULL: all), the first prompt_len[b] (NULL: 0) of
- *                                       them being the prompt; fewer than 2^30 entries
+ *                                       them being the prompt; fewer than 2^28 entries
  *   draft        [B, S] i32             NULL: none
  *   bias_ids     [B, nbias] i32, bias_values [B, nbias] f32   NULL: none
  *   mask         [B, S, ceil(V / 32)] u32   NULL: none
  * Ids outside [0, V) are skipped (padding).  p must not overlap an input.
+ * workspace: dsa_probs_workspace_size bytes (history_cap 0 without a history), 256-byte aligned,
+ * written by every call (calls that overlap on the GPU need one each).  S <= 65535,
+ * nbias < 2^28.
  */
+size_t dsa_probs_workspace_size(int B, int S, int V, int history_cap, int nbias);
 dsa_status dsa_logits_probs(const void *logits, int dtype, int B, int S, int V, const float *temperature,
                             const float *repetition, const float *frequency, const float *presence,
                             const int32_t *history, int history_cap, const int32_t *history_len,
                             const int32_t *prompt_len, const int32_t *draft, const int32_t *bias_ids,
                             const float *bias_values, int nbias, const uint32_t *mask, float *p,
-                            cudaStream_t stream);
+                            void *workspace, size_t workspace_bytes, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -35,7 +35,8 @@ EXPORTS = ("dsa_status_string", "dsa_version", "dsa_workspace_size", "dsa_worksp
            "dsa_sparse_attn", "dsa_group_forward", "dsa_topk_noalloc", "dsa_device_error",
            "dsa_check_device_status", "dsa_last_cuda_error", "dsa_cuda_error_string", "dsa_verify",
            "dsa_decode_workspace_size", "dsa_decode_step", "dsa_rope_init", "dsa_rope", "dsa_cache_append",
-           "dsa_paged_workspace_size", "dsa_paged_attn", "dsa_logits_probs")
+           "dsa_paged_workspace_size", "dsa_paged_attn", "dsa_probs_workspace_size",
+           "dsa_logits_probs")
 
 ROPE_LAYOUTS = ("half", "interleaved")  # DSA_ROPE_HALF, DSA_ROPE_INTERLEAVED
 
@@ -108,7 +109,9 @@ def lib() -> ctypes.CDLL:
         L.dsa_paged_workspace_size.argtypes = [I, I, I]
         L.dsa_paged_workspace_size.restype = S
         L.dsa_paged_attn.argtypes = [P, P, P, P, P, I, I, I, I, I, I, F, P, P, P, S, P]
-        L.dsa_logits_probs.argtypes = [P, I, I, I, I, P, P, P, P, P, I, P, P, P, P, P, I, P, P, P]
+        L.dsa_probs_workspace_size.argtypes = [I, I, I, I, I]
+        L.dsa_probs_workspace_size.restype = S
+        L.dsa_logits_probs.argtypes = [P, I, I, I, I, P, P, P, P, P, I, P, P, P, P, P, I, P, P, P, S, P]
         for f in ("dsa_rope_init", "dsa_rope", "dsa_cache_append", "dsa_paged_attn", "dsa_logits_probs"):
             getattr(L, f).restype = I
         for f in ("dsa_index_score", "dsa_index_score_e4m3", "dsa_sparse_attn_shard", "dsa_shard_candidates",
@@ -589,7 +592,7 @@ def dsa_paged_attn(q, cache, table, cu_q, ctx_len, scale: float, out=None, lse=N
 
 def dsa_logits_probs(logits, temperature=None, history=None, history_len=None, prompt_len=None, draft=None,
                      repetition=None, frequency=None, presence=None, bias_ids=None, bias_values=None, mask=None, out=None,
-                     stream=None):
+                     ws=None, stream=None):
     """logits [B, S, V] f32 or bf16 -> p [B, S, V] f32 for dsa_verify (see include/dsa.h):
     penalties over history [B, cap] int32 (its first history_len[b], of which prompt_len[b]
     are the prompt) and the drafts before a row (draft [B, S] int32), biases (bias_ids and
@@ -618,5 +621,10 @@ def dsa_logits_probs(logits, temperature=None, history=None, history_len=None, p
             _arg(bias_ids, i32, (B, nb), "bias_ids", dev), _arg(bias_values, f32, (B, nb), "bias_values", dev), nb,
             _arg(mask, i32, (B, S, (V + 31) // 32), "mask", dev), _arg(out, f32, (B, S, V), "out", dev))
     if B and S:
+        if ws is None:
+            ws = torch.empty(lib().dsa_probs_workspace_size(B, S, V, cap, nb), dtype=torch.uint8, device=dev)
+        elif ws.device != dev:
+            raise ValueError(f"workspace is on {ws.device}, expected {dev}")
+        args += (_ptr(ws, (torch.uint8,), "workspace"), ws.numel())
         _call("dsa_logits_probs", dev, stream, *args)
     return out

@@ -605,16 +605,24 @@ dsa_status dsa_paged_attn(const uint16_t* q, const uint16_t* cache, const int32_
   return cuda_status(launch_paged_attn(q, cache, pb, H, scale, out, lse, workspace, stream));
 }
 
+size_t dsa_probs_workspace_size(int B, int S, int V, int history_cap, int nbias) {
+  if (B <= 0 || S <= 0 || S > 65535 || V <= 0 || V >= (1 << 24) || (long long)B * S > 0x7FFFFFFFLL || history_cap < 0 ||
+      history_cap >= (1 << 28) || nbias < 0 || nbias >= (1 << 28))
+    return 0;
+  return probs_workspace_bytes(B, S, V, history_cap, nbias);
+}
+
 dsa_status dsa_logits_probs(const void* logits, int dtype, int B, int S, int V, const float* temperature,
                             const float* repetition, const float* frequency, const float* presence,
                             const int32_t* history, int history_cap, const int32_t* history_len,
                             const int32_t* prompt_len, const int32_t* draft, const int32_t* bias_ids,
-                            const float* bias_values, int nbias, const uint32_t* mask, float* p, cudaStream_t stream) {
+                            const float* bias_values, int nbias, const uint32_t* mask, float* p, void* workspace,
+                            size_t workspace_bytes, cudaStream_t stream) {
   if (!logits || !p || B < 0 || S < 0 || V <= 0 || V >= (1 << 24) || history_cap < 0 || nbias < 0 ||
       (long long)B * S > 0x7FFFFFFFLL || (nbias > 0 && (!bias_ids || !bias_values)))
     return DSA_ERR_INVALID_ARG;
   if (dtype != DSA_BF16 && dtype != DSA_F32) return DSA_ERR_UNSUPPORTED;
-  if (history_cap >= (1 << 30)) return DSA_ERR_UNSUPPORTED;
+  if (history_cap >= (1 << 28) || nbias >= (1 << 28) || S > 65535) return DSA_ERR_UNSUPPORTED;
   if (!aligned(logits, dtype == DSA_F32 ? 4 : 2)) return DSA_ERR_INVALID_ARG;
   const void* words[] = {p,       temperature, repetition, frequency, presence,    history,
                          history_len, prompt_len,  draft,      bias_ids,  bias_values, mask};
@@ -641,7 +649,10 @@ dsa_status dsa_logits_probs(const void* logits, int dtype, int B, int S, int V, 
   a.V = V;
   a.history_cap = history_cap;
   a.nbias = nbias;
-  return cuda_status(launch_probs(a, stream));
+  if (!workspace || workspace_bytes < probs_workspace_bytes(B, S, V, history ? history_cap : 0, nbias) ||
+      !aligned(workspace, 256))
+    return DSA_ERR_WORKSPACE;
+  return cuda_status(launch_probs(a, workspace, stream));
 }
 
 }  // extern "C"

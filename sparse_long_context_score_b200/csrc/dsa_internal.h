@@ -177,6 +177,7 @@ struct ProbsArgs {
   const uint32_t* mask;      // [B][S][ceil(V / 32)]
   int dtype, B, S, V, history_cap, nbias;
 };
-cudaError_t launch_probs(const ProbsArgs& a, cudaStream_t stream);
+size_t probs_workspace_bytes(int B, int S, int V, int history_cap, int nbias);
+cudaError_t launch_probs(const ProbsArgs& a, void* workspace, cudaStream_t stream);
 
 }  // namespace dsa

@@ -8,118 +8,554 @@
 //   z = -inf                              v's mask bit is 0, or z is NaN
 //   p = exp((z - max z) / T) / sum        T > 0; else 1 at the lowest index of the maximum
 // A row that its mask leaves empty gets zeros.
+//
+// Two passes over chunks of 4096 entries: the first forms each chunk's maximum and sum (or the
+// place of its maximum), the second joins the row's chunks and writes p.  The second reads the
+// logits from L2: sequences are taken in groups whose logits fit there.  A CTA takes its chunk
+// for several rows of a sequence, with the next row's logits in flight.
+// The entries that the history, the drafts and the biases name are few and lie anywhere, and what
+// they cost must not be paid by all: the first pass gathers them and takes them out of the dense
+// stream by a bit each; a kernel behind it adds their share to the row's sums, and one behind the
+// second pass puts their probabilities over what that wrote there, a thread an entry.
+// 16 x 7 rows of 151552 (68 MB of logits, 68 MB of p), us, without lists / with 4096 tokens of
+// history, 32 biases and a mask: 34 / 62.  Tried: a row held in the registers of a cluster of
+// eight CTAs, one pass (83 / 133: one such CTA fills an SM, and its loads, lists, exchanges and
+// stores follow one another); lists as a number and a bit for every entry (34 / 82: a warp does
+// the repetition's arithmetic wherever one of its lanes needs it); the listed entries treated by
+// their chunk's CTA, row by row (34 / 144) or behind all rows (34 / 114): most of a history lies
+// in one chunk.
 #include <cuda_bf16.h>
 
 #include "dsa_common.cuh"
 #include "dsa_internal.h"
+#include "sm100.cuh"
 
 namespace dsa {
 namespace {
 
-// What is known of an entry before its logit is read, one word an entry: how often it was
-// generated, whether it was seen at all, and whether a bias names it.
-constexpr uint32_t kSeen = 0x80000000u, kBiased = 0x40000000u, kCount = 0x3FFFFFFFu;
+// What is known of an entry while the lists are gathered: how often it was generated (drafts
+// aside), whether it was seen at all, and whether a bias or a draft names it.
+constexpr uint32_t kSeen = 0x80000000u, kBiased = 0x40000000u, kDrafted = 0x20000000u, kCount = 0x1FFFFFFFu;
 
-__device__ __forceinline__ float adjust(float z, uint32_t word, const ProbsArgs& a, int b, int v, float rep, float freq,
-                                        float pres) {
-  if (word & kSeen) z = z > 0.f ? z / rep : z * rep;
-  const uint32_t count = word & kCount;
-  if (count) z = z - freq * (float)count - pres;
-  if (word & kBiased) {
-    float s = 0.f;
-    for (int i = 0; i < a.nbias; ++i)
-      if (a.bias_ids[(size_t)b * a.nbias + i] == v) s += a.bias_values[(size_t)b * a.nbias + i];
-    z += s;
+constexpr double kL2Bytes = 72e6;  // of 126 MB, beside the probabilities that leave through it
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// One pair of a chunk or a row: the largest logit and the sum of exp((z - m) / T) -- where the
+// temperature asks for the maximum alone, the lowest index at it.
+struct Partial {
+  float m, s;
+};
+constexpr float kNoPlace = 1e9f;  // behind every entry (places are below 2^24: exact in f32)
+
+// Weights are 2^((z - m) c), c = log2(e) / T, wherever m is finite and c is neither zero nor
+// infinite.  Other rows (an infinite maximum, temperatures outside the normal range): entries at
+// the maximum count as 1 and the others not at all -- but for T = inf, where all above -inf count
+// as 1.
+__device__ __forceinline__ bool ordinary(float m, float c) { return fabsf(m) < INFINITY && c > 0.f && c < INFINITY; }
+__device__ __forceinline__ bool counts_as_one(float z, float m, float c) {
+  return c == 0.f && m != INFINITY ? z != -INFINITY : z == m;
+}
+
+// The partials of a warp's lanes as one, in every lane.
+__device__ __forceinline__ Partial warp_join(Partial x, float c, bool greedy) {
+  float m = x.m;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  if (greedy) {
+    float first = x.m == m ? x.s : kNoPlace;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) first = fminf(first, __shfl_xor_sync(0xFFFFFFFFu, first, o));
+    return {m, first};
   }
-  return z != z ? -INFINITY : z;
+  float s = 0.f;
+  if (x.m != -INFINITY) s = ordinary(m, c) ? x.s * exp2_approx((x.m - m) * c) : counts_as_one(x.m, m, c) ? x.s : 0.f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+  return {m, s};
 }
 
-__device__ __forceinline__ float load_logit(const void* p, size_t i, int dtype) {
-  return dtype == DSA_F32 ? static_cast<const float*>(p)[i] : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kItems = 16;                  // entries of a thread
+constexpr int kChunk = kThreads * kItems;   // 4096
+constexpr int kBlocks = 4;                  // CTAs of an SM
+constexpr int kRowBlock = 64;               // rows whose partials are joined at once
+
+// The chunk's entry that item i of this thread is: four in a row where rows start on a vector
+// (16 bytes of f32, 8 of bf16), else neighbours in neighbouring threads.
+template <bool kVector>
+__device__ __forceinline__ int place(int i) {
+  return kVector ? 4 * (kThreads * (i / 4) + (int)threadIdx.x) + i % 4 : kThreads * i + (int)threadIdx.x;
+}
+__device__ __forceinline__ float load_f32(const float* p) { return *p; }
+__device__ __forceinline__ float load_f32(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+
+template <class T, bool kVector, bool kOnce>
+__device__ __forceinline__ void load_row(const T* row, int v0, int v1, float (&z)[kItems]) {
+  if constexpr (kVector) {
+#pragma unroll
+    for (int i = 0; i < kItems; i += 4) {
+      const int v = v0 + place<true>(i);
+      if (v < v1) {  // (V is a multiple of four)
+        if constexpr (sizeof(T) == 4) {
+          const float4* p = reinterpret_cast<const float4*>(row + v);
+          const float4 x = kOnce ? __ldcs(p) : *p;
+          z[i] = x.x, z[i + 1] = x.y, z[i + 2] = x.z, z[i + 3] = x.w;
+        } else {
+          const uint2* p = reinterpret_cast<const uint2*>(row + v);
+          const uint2 x = kOnce ? __ldcs(p) : *p;
+          z[i] = __uint_as_float(x.x << 16), z[i + 1] = __uint_as_float(x.x & 0xFFFF0000u);
+          z[i + 2] = __uint_as_float(x.y << 16), z[i + 3] = __uint_as_float(x.y & 0xFFFF0000u);
+        }
+      } else {
+        z[i] = z[i + 1] = z[i + 2] = z[i + 3] = -INFINITY;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+      const int v = v0 + place<false>(i);
+      z[i] = v < v1 ? load_f32(row + v) : -INFINITY;
+    }
+  }
 }
 
-constexpr int kThreads = 1024;
+// A listed entry of a sequence.
+struct Listed {
+  uint32_t v;      // the entry; kSeen, kBiased; kNobody: a gap
+  uint32_t count;  // how often it was generated, drafts aside
+  float bias;      // sum of its biases
+};
+constexpr uint32_t kNobody = 0xFFFFFFFFu, kEntry = 0xFFFFFFu;
+// What the first pass leaves for the others: a sequence's listed entries chunk after chunk, with
+// gaps -- a chunk's start where they do if every name in the lists were another entry.
+struct Lists {
+  Listed* entries;  // [B][room]
+  int room;         // names in the lists of a sequence at most, rounded up to whole CTAs
+};
 
-template <class F>
-__device__ __forceinline__ float block_reduce(float v, float* s, F f) {
-  for (int o = 16; o > 0; o >>= 1) v = f(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-  __syncthreads();
-  if (threadIdx.x % 32 == 0) s[threadIdx.x / 32] = v;
-  __syncthreads();
-  v = s[threadIdx.x % 32];
-  for (int o = 16; o > 0; o >>= 1) v = f(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-  return v;
+struct RowSettings {
+  float rep, freq, pres, c;
+  bool greedy;
+};
+__device__ __forceinline__ RowSettings row_settings(const ProbsArgs& a, int b) {
+  const float temperature = a.temperature ? a.temperature[b] : 1.f;
+  return {a.repetition ? a.repetition[b] : 1.f, a.frequency ? a.frequency[b] : 0.f, a.presence ? a.presence[b] : 0.f,
+          1.4426950408889634f / temperature, !(temperature > 0.f)};
 }
 
-// One block per row.  The row of p holds, in turn, the words of the entries, their
-// adjusted logits and their probabilities.
-__global__ void __launch_bounds__(kThreads) probs_kernel(const __grid_constant__ ProbsArgs a) {
-  __shared__ float s_red[32];
-  const int row = blockIdx.x, b = row / a.S, j = row - b * a.S, V = a.V;
-  float* p = a.p + (size_t)row * V;
-  uint32_t* words = reinterpret_cast<uint32_t*>(p);
-  for (int v = threadIdx.x; v < V; v += kThreads) words[v] = 0u;
+// Two partials as one.
+__device__ __forceinline__ Partial lane_join(Partial x, Partial y, float c, bool greedy) {
+  const float m = fmaxf(x.m, y.m);
+  if (greedy) return {m, fminf(x.m == m ? x.s : kNoPlace, y.m == m ? y.s : kNoPlace)};
+  const bool usual = ordinary(m, c);
+  auto share = [&](const Partial& p) {
+    if (p.m == -INFINITY) return 0.f;
+    return usual ? p.s * exp2_approx((p.m - m) * c) : counts_as_one(p.m, m, c) ? p.s : 0.f;
+  };
+  return {m, share(x) + share(y)};
+}
+// A row's partials as one, in every lane of the warp.
+__device__ __forceinline__ Partial join_row(const Partial* partials, int parts, float c, bool greedy) {
+  Partial x{-INFINITY, greedy ? kNoPlace : 0.f};
+#pragma unroll 4
+  for (int i = threadIdx.x & 31; i < parts; i += 32) {
+    const float2 y = __ldcg(reinterpret_cast<const float2*>(partials) + i);
+    x = lane_join(x, {y.x, y.y}, c, greedy);
+  }
+  return warp_join(x, c, greedy);
+}
+
+// A row's partial over the CTA, from each warp's; in the lanes of one warp (true there).
+__device__ __forceinline__ bool block_join(Partial& x, int j, float c, bool greedy, Partial* s_part) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  Partial* slot = s_part + (j & 1) * kWarps;
+  if (lane == 0) slot[warp] = x;
   __syncthreads();
+  if (warp != j % kWarps) return false;
+  x = warp_join(lane < kWarps ? slot[lane] : Partial{-INFINITY, greedy ? kNoPlace : 0.f}, c, greedy);
+  return true;
+}
+
+// The shared memory that gathers a chunk's listed entries.
+struct Gathered {
+  uint32_t words[kChunk];  // by entry
+  int number, names, below;  // listed entries; names in the chunk, and in those before
+};
+// s_bias: by entry, where biases are given
+__device__ __forceinline__ void gather(const ProbsArgs& a, int b, int v0, int v1, Gathered& g, float* s_bias) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  for (int i = tid; i < kChunk / 4; i += kThreads) reinterpret_cast<uint4*>(g.words)[i] = make_uint4(0, 0, 0, 0);
+  if (tid == 0) g.number = g.names = g.below = 0;
+  __syncthreads();
+  int below = 0, names = 0;
   if (a.history) {
     const int len = a.history_len ? min(a.history_len[b], a.history_cap) : a.history_cap;
     const int prompt = a.prompt_len ? a.prompt_len[b] : 0;
-    for (int i = threadIdx.x; i < len; i += kThreads) {
-      const int v = a.history[(size_t)b * a.history_cap + i];
-      if (v < 0 || v >= V) continue;
-      atomicOr(&words[v], kSeen);
-      if (i >= prompt) atomicAdd(&words[v], 1u);
+    const int32_t* list = a.history + (size_t)b * a.history_cap;
+#pragma unroll 8
+    for (int i = tid; i < len; i += kThreads) {
+      const int v = list[i];
+      below += v >= 0 && v < v0;
+      if (v < v0 || v >= v1) continue;
+      ++names;
+      atomicOr(&g.words[v - v0], kSeen);
+      if (i >= prompt) atomicAdd(&g.words[v - v0], 1u);
     }
   }
   if (a.draft)
-    for (int i = threadIdx.x; i < j; i += kThreads) {
+    for (int i = tid; i < a.S - 1; i += kThreads) {
       const int v = a.draft[(size_t)b * a.S + i];
-      if (v < 0 || v >= V) continue;
-      atomicOr(&words[v], kSeen);
-      atomicAdd(&words[v], 1u);
+      below += v >= 0 && v < v0;
+      if (v < v0 || v >= v1) continue;
+      ++names;
+      atomicOr(&g.words[v - v0], kDrafted);
     }
-  for (int i = threadIdx.x; i < a.nbias; i += kThreads) {
-    const int v = a.bias_ids[(size_t)b * a.nbias + i];
-    if (v >= 0 && v < V) atomicOr(&words[v], kBiased);
+  // a warp sums an entry's biases in the list's order, so that equal ids always sum alike
+  const int32_t* ids = a.bias_ids + (size_t)b * a.nbias;
+  const float* values = a.bias_values + (size_t)b * a.nbias;
+  for (int i0 = 32 * warp; i0 < a.nbias; i0 += kThreads) {
+    const int own = i0 + lane < a.nbias ? ids[i0 + lane] : -1;
+    below += own >= 0 && own < v0;
+    names += own >= v0 && own < v1;
+    for (uint32_t todo = __ballot_sync(0xFFFFFFFFu, own >= v0 && own < v1); todo; todo &= todo - 1) {
+      const int v = __shfl_sync(0xFFFFFFFFu, own, __ffs(todo) - 1);
+      float sum = 0.f;
+      for (int k0 = 0; k0 < a.nbias; k0 += 32) {
+        const bool same = k0 + lane < a.nbias && ids[k0 + lane] == v;
+        const float value = same ? values[k0 + lane] : 0.f;
+        for (uint32_t hits = __ballot_sync(0xFFFFFFFFu, same); hits; hits &= hits - 1)
+          sum += __shfl_sync(0xFFFFFFFFu, value, __ffs(hits) - 1);
+      }
+      if (lane == 0) {
+        s_bias[v - v0] = sum;
+        atomicOr(&g.words[v - v0], kBiased);
+      }
+    }
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    below += __shfl_xor_sync(0xFFFFFFFFu, below, o);
+    names += __shfl_xor_sync(0xFFFFFFFFu, names, o);
+  }
+  if (lane == 0 && below) atomicAdd(&g.below, below);
+  if (lane == 0 && names) atomicAdd(&g.names, names);
   __syncthreads();
-  const float rep = a.repetition ? a.repetition[b] : 1.f, freq = a.frequency ? a.frequency[b] : 0.f;
-  const float pres = a.presence ? a.presence[b] : 0.f, T = a.temperature ? a.temperature[b] : 1.f;
-  const uint32_t* mask = a.mask ? a.mask + (size_t)row * ((V + 31) / 32) : nullptr;
-  float m = -INFINITY;
-  for (int v = threadIdx.x; v < V; v += kThreads) {
-    float z = adjust(load_logit(a.logits, (size_t)row * V + v, a.dtype), words[v], a, b, v, rep, freq, pres);
-    if (mask && !((mask[v >> 5] >> (v & 31)) & 1u)) z = -INFINITY;
-    p[v] = z;
-    m = fmaxf(m, z);
+}
+
+// The listed entries: their partials (kWrite false), or their probabilities, over those that the
+// second pass wrote there.  CTA (256 of a sequence's entries, sequence b0 + blockIdx.y, four rows).
+constexpr int kListedRows = 4;
+template <class T, bool kWrite>
+__global__ void __launch_bounds__(kThreads) probs_listed_kernel(const __grid_constant__ ProbsArgs a, int b0, int chunks,
+                                                                Lists lists, Partial* partials) {
+  __shared__ Partial s_part[kListedRows][kWarps];
+  const int e = blockIdx.x, parts = chunks + gridDim.x, b = b0 + blockIdx.y, V = a.V;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int j0 = blockIdx.z * kListedRows, rows = min(a.S - j0, kListedRows);
+  const size_t row0 = (size_t)b * a.S + j0;
+  // The second of these kernels starts when all CTAs of the second pass are past their wait, which
+  // the lists and the partials are complete behind: it waits for that pass only where it writes.
+  if (!kWrite) {
+    sm100::grid_dep_wait();
+    sm100::grid_dep_launch();
   }
-  m = block_reduce(m, s_red, [](float x, float y) { return fmaxf(x, y); });
-  if (m == -INFINITY) {
-    for (int v = threadIdx.x; v < V; v += kThreads) p[v] = 0.f;
-    return;
-  }
-  const bool greedy = !(T > 0.f);
-  const float c = 1.4426950408889634f / T;
-  // (entries at the maximum count as 1 whatever the temperature; -inf never counts)
-  auto weight = [&](float z) { return z == m ? 1.f : z == -INFINITY ? 0.f : exp2f((z - m) * c); };
-  float sum = 0.f, first = (float)V;
-  for (int v = threadIdx.x; v < V; v += kThreads) {
-    if (greedy) {
-      if (p[v] == m) first = fminf(first, (float)v);
+  const Listed* entry = lists.entries + (size_t)b * lists.room + kThreads * e + threadIdx.x;
+  const uint32_t word = __ldcg(&entry->v), generated = __ldcg(&entry->count);
+  const float given = __ldcg(&entry->bias);
+  const bool there = word != kNobody;
+  const int v = there ? (int)(word & kEntry) : 0;
+  const RowSettings set = row_settings(a, b);
+  if (__syncthreads_or(there)) {
+    float z[kListedRows];
+    uint32_t bits = 0xFu;  // of the mask, a row each
+#pragma unroll
+    for (int i = 0; i < kListedRows; ++i) {
+      z[i] = there && i < rows ? load_f32(static_cast<const T*>(a.logits) + (row0 + i) * V + v) : -INFINITY;
+      if (a.mask && there && i < rows && !((a.mask[(row0 + i) * ((V + 31) / 32) + (v >> 5)] >> (v & 31)) & 1u)) bits &= ~(1u << i);
+    }
+    uint32_t count = there ? generated : 0u;
+    const float bias = there && (word & kBiased) ? given : 0.f;
+    if (a.draft)
+      for (int k = 0; k < j0; ++k) count += a.draft[(size_t)b * a.S + k] == v;
+#pragma unroll
+    for (int i = 0; i < kListedRows; ++i) {
+      if (a.draft && i > 0 && i < rows) count += a.draft[row0 + i - 1] == v;
+      float x = z[i];
+      if ((word & kSeen) || count) x = x > 0.f ? x / set.rep : x * set.rep;
+      if (count) x = x - set.freq * (float)count - set.pres;
+      x += bias;
+      z[i] = there && ((bits >> i) & 1u) ? fmaxf(x, -INFINITY) : -INFINITY;  // NaN becomes -inf
+    }
+    if constexpr (!kWrite) {
+#pragma unroll
+      for (int i = 0; i < kListedRows; ++i) {
+        const Partial y =
+            warp_join({z[i], set.greedy ? (there ? (float)v : kNoPlace) : z[i] == -INFINITY ? 0.f : 1.f}, set.c, set.greedy);
+        if (lane == 0) s_part[i][warp] = y;
+      }
     } else {
-      sum += weight(p[v]);
+      if (warp < rows) {
+        const Partial y = join_row(partials + (row0 + warp) * parts, parts, set.c, set.greedy);
+        if (lane == 0) s_part[warp][0] = y;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kListedRows; ++i) {
+        const Partial y = s_part[i][0];
+        if (i >= rows || y.m == -INFINITY) z[i] = 0.f;
+        else if (set.greedy) z[i] = (float)v == y.s ? 1.f : 0.f;
+        else z[i] = (ordinary(y.m, set.c) ? exp2_approx((z[i] - y.m) * set.c) : counts_as_one(z[i], y.m, set.c) ? 1.f : 0.f) / y.s;
+      }
+      sm100::grid_dep_wait();
+#pragma unroll
+      for (int i = 0; i < kListedRows; ++i)
+        if (there && i < rows) a.p[(row0 + i) * V + v] = z[i];
+    }
+  } else if (!kWrite && threadIdx.x < kListedRows * kWarps) {  // nothing but gaps
+    s_part[threadIdx.x / kWarps][threadIdx.x % kWarps] = Partial{-INFINITY, set.greedy ? kNoPlace : 0.f};
+  }
+  if constexpr (!kWrite) {
+    __syncthreads();
+    if (warp < rows) {
+      const Partial y =
+          warp_join(lane < kWarps ? s_part[warp][lane] : Partial{-INFINITY, set.greedy ? kNoPlace : 0.f}, set.c, set.greedy);
+      if (lane == 0) partials[(row0 + warp) * parts + chunks + e] = y;
     }
   }
-  sum = block_reduce(sum, s_red, [](float x, float y) { return x + y; });
-  first = block_reduce(first, s_red, [](float x, float y) { return fminf(x, y); });
-  for (int v = threadIdx.x; v < V; v += kThreads)
-    p[v] = greedy ? ((float)v == first ? 1.f : 0.f) : weight(p[v]) / sum;
+}
+
+// Pass 1 (kWrite false): partials[row][parts], those of the chunks, without the listed entries
+// (kLists).  Pass 2: p of all entries, from the row's partials; the listed ones' is put right
+// behind it.  CTA (chunk, sequence b0 + blockIdx.y, rows rows_each blockIdx.z ...).
+template <class T, bool kVector, bool kLists, bool kWrite>
+__global__ void __launch_bounds__(kThreads, kBlocks) probs_kernel(const __grid_constant__ ProbsArgs a, int b0, int rows_each,
+                                                                  int parts, Lists lists, Partial* partials) {
+  __shared__ __align__(16) unsigned char s_gathered[kLists && !kWrite ? sizeof(Gathered) : 16];
+  __shared__ Partial s_part[kWrite ? kRowBlock : 2 * kWarps];
+  extern __shared__ float s_bias[];
+  Gathered& g = *reinterpret_cast<Gathered*>(s_gathered);
+  const int chunk = blockIdx.x, b = b0 + blockIdx.y, V = a.V, S = a.S;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int j0 = blockIdx.z * rows_each, j1 = min(S, j0 + rows_each);
+  const size_t row0 = (size_t)b * S;
+  const int v0 = chunk * kChunk, v1 = min(V, v0 + kChunk);
+  const T* logits = static_cast<const T*>(a.logits) + row0 * V;
+  float next[kItems];
+  load_row<T, kVector, kWrite>(logits + (size_t)j0 * V, v0, v1, next);
+  if (kWrite) sm100::grid_dep_wait();  // the partials
+  sm100::grid_dep_launch();
+  const RowSettings set = row_settings(a, b);
+  const float c = set.c;
+  const bool greedy = set.greedy;
+  uint32_t listed = 0;  // which of this thread's entries are
+  if constexpr (kLists && !kWrite) {
+    gather(a, b, v0, v1, g, s_bias);
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) listed |= (g.words[place<kVector>(i)] != 0u ? 1u : 0u) << i;
+    if (blockIdx.z == 0) {
+      Listed* out = lists.entries + (size_t)b * lists.room + g.below;
+      int at = listed ? atomicAdd(&g.number, __popc(listed)) : 0;  // (the order within a chunk does not matter)
+      for (uint32_t todo = listed; todo; todo &= todo - 1) {
+        const uint32_t e = place<kVector>(__ffs(todo) - 1), word = g.words[e];
+        out[at++] = {(v0 + e) | (word & (kSeen | kBiased)), word & kCount, word & kBiased ? s_bias[e] : 0.f};
+      }
+      __syncthreads();
+      // gaps: behind this chunk's entries, and behind the last chunk's
+      const int end = chunk == (int)gridDim.x - 1 ? lists.room - g.below : g.names;
+      for (int i = g.number + threadIdx.x; i < end; i += kThreads) out[i].v = kNobody;
+    }
+  }
+  // the mask's bits of a row, by entry, without the listed entries; loaded a row ahead
+  auto load_bits = [&](int j) {
+    uint32_t bits = ~listed;
+    if (a.mask) {
+      const uint32_t* mask = a.mask + (row0 + j) * ((V + 31) / 32);
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < kItems; i += kVector ? 4 : 1) {  // (four in a row lie in one word)
+        const int v = v0 + place<kVector>(i);
+        m |= ((v < v1 ? mask[v >> 5] >> (v & 31) : 0u) & (kVector ? 15u : 1u)) << i;
+      }
+      bits &= m;
+    }
+    return bits;
+  };
+  uint32_t next_bits = load_bits(j0);
+  for (int j = j0; j < j1; ++j) {
+    const size_t row = row0 + j;
+    if constexpr (kWrite) {
+      if ((j - j0) % kRowBlock == 0) {
+        __syncthreads();
+        for (int r = j + warp; r < min(j1, j + kRowBlock); r += kWarps) {
+          const Partial x = join_row(partials + (row0 + r) * parts, parts, c, greedy);
+          if (lane == 0) s_part[r - j] = x;
+        }
+        __syncthreads();
+      }
+    }
+    float z[kItems];
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) z[i] = next[i];
+    const uint32_t bits = next_bits;
+    if (j + 1 < j1) {
+      load_row<T, kVector, kWrite>(logits + (size_t)(j + 1) * V, v0, v1, next);
+      next_bits = load_bits(j + 1);
+    }
+    if (a.mask || (kLists && !kWrite)) {  // the dense stream goes on without the masked and the listed entries
+#pragma unroll
+      for (int i = 0; i < kItems; ++i)
+        if (!((bits >> i) & 1u)) z[i] = -INFINITY;
+    }
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) z[i] = fmaxf(z[i], -INFINITY);  // NaN becomes -inf
+    if constexpr (!kWrite) {
+      Partial x{-INFINITY, greedy ? kNoPlace : 0.f};
+#pragma unroll
+      for (int i = 0; i < kItems; ++i) x.m = fmaxf(x.m, z[i]);
+      // (a warp's maximum, so that its lanes' sums add up without weights)
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) x.m = fmaxf(x.m, __shfl_xor_sync(0xFFFFFFFFu, x.m, o));
+      if (greedy) {
+#pragma unroll
+        for (int i = 0; i < kItems; ++i)
+          if (z[i] == x.m) x.s = fminf(x.s, (float)(v0 + place<kVector>(i)));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) x.s = fminf(x.s, __shfl_xor_sync(0xFFFFFFFFu, x.s, o));
+      } else if (x.m != -INFINITY) {
+        float m = x.m, scale = c;
+        if (!ordinary(m, c)) {
+#pragma unroll
+          for (int i = 0; i < kItems; ++i) z[i] = counts_as_one(z[i], x.m, c) ? 0.f : -INFINITY;
+          m = 0.f;
+          scale = 1.f;
+        }
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) x.s += exp2_approx((z[i] - m) * scale);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) x.s += __shfl_xor_sync(0xFFFFFFFFu, x.s, o);
+      }
+      if (block_join(x, j, c, greedy, s_part) && lane == 0) partials[row * parts + chunk] = x;
+    } else {
+      const Partial x = s_part[(j - j0) % kRowBlock];
+      const bool usual = ordinary(x.m, c);
+      const float m = usual ? x.m : 0.f, scale = usual ? c : 1.f, share = 1.f / x.s;
+      if (x.m == -INFINITY) {
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) z[i] = 0.f;
+      } else if (greedy) {
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) z[i] = (float)(v0 + place<kVector>(i)) == x.s ? 1.f : 0.f;
+      } else {
+        if (!usual) {
+#pragma unroll
+          for (int i = 0; i < kItems; ++i) z[i] = counts_as_one(z[i], x.m, c) ? 0.f : -INFINITY;
+        }
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) z[i] = exp2_approx((z[i] - m) * scale) * share;
+      }
+      float* p = a.p + row * V;
+#pragma unroll
+      for (int i = 0; i < kItems; i += kVector ? 4 : 1) {
+        const int v = v0 + place<kVector>(i);
+        if (v >= v1) continue;
+        if constexpr (kVector) {
+          __stcs(reinterpret_cast<float4*>(p + v), make_float4(z[i], z[i + 1], z[i + 2], z[i + 3]));
+        } else {
+          __stcs(p + v, z[i]);
+        }
+      }
+    }
+  }
+}
+
+struct ProbsLayout {
+  size_t partials, entries, total;
+  int chunks, room;
+};
+ProbsLayout probs_layout(int B, int S, int V, int history_cap, int nbias) {
+  ProbsLayout l;
+  l.chunks = (V + kChunk - 1) / kChunk;
+  l.room = (history_cap + S + nbias + kThreads - 1) / kThreads * kThreads;
+  l.partials = 0;
+  l.entries = ((size_t)B * S * (l.chunks + l.room / kThreads) * sizeof(Partial) + 255) & ~(size_t)255;
+  l.total = l.entries + (size_t)B * l.room * sizeof(Listed);
+  return l;
+}
+
+template <class T, bool kVector, bool kLists>
+cudaError_t launch_passes(const ProbsArgs& a, unsigned char* ws, cudaStream_t stream) {
+  const int sms = device_sm_count();
+  if (sms <= 0) return cudaErrorInvalidDevice;
+  const ProbsLayout l = probs_layout(a.B, a.S, a.V, a.history ? a.history_cap : 0, a.nbias);
+  const int entry_parts = kLists ? l.room / kThreads : 0, parts = l.chunks + entry_parts;
+  Partial* partials = reinterpret_cast<Partial*>(ws + l.partials);
+  const Lists lists{reinterpret_cast<Listed*>(ws + l.entries), l.room};
+  // sequences whose logits stay in L2 between the passes, and that the grid can number
+  const double each = (double)a.S * a.V * sizeof(T);
+  int group = each >= kL2Bytes ? 1 : (int)(kL2Bytes / each);
+  if (group > 65535) group = 65535;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // waits in-kernel
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  for (int b0 = 0; b0 < a.B; b0 += group) {
+    const int n = a.B - b0 < group ? a.B - b0 : group;
+    // rows of a CTA: as many as leave a CTA for each place on the GPU
+    long long rows_each = (long long)l.chunks * n * a.S / ((long long)kBlocks * sms);
+    rows_each = rows_each < 1 ? 1 : rows_each > a.S ? a.S : rows_each;
+    const dim3 grid(l.chunks, n, (unsigned)((a.S + rows_each - 1) / rows_each));
+    const dim3 entry_grid(entry_parts, n, (a.S + kListedRows - 1) / kListedRows);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cfg.dynamicSmemBytes = kLists && a.nbias > 0 ? kChunk * sizeof(float) : 0;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, probs_kernel<T, kVector, kLists, false>, a, b0, (int)rows_each, parts, lists, partials);
+    if (e != cudaSuccess) return e;
+    cfg.dynamicSmemBytes = 0;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (kLists) {
+      cfg.gridDim = entry_grid;
+      if ((e = cudaLaunchKernelEx(&cfg, probs_listed_kernel<T, false>, a, b0, l.chunks, lists, partials)) != cudaSuccess)
+        return e;
+      cfg.gridDim = grid;
+    }
+    if ((e = cudaLaunchKernelEx(&cfg, probs_kernel<T, kVector, false, true>, a, b0, (int)rows_each, parts, lists, partials)) !=
+        cudaSuccess)
+      return e;
+    if (kLists) {
+      cfg.gridDim = entry_grid;
+      if ((e = cudaLaunchKernelEx(&cfg, probs_listed_kernel<T, true>, a, b0, l.chunks, lists, partials)) != cudaSuccess) return e;
+    }
+  }
+  return cudaSuccess;
+}
+
+template <class T, bool kVector>
+cudaError_t launch(const ProbsArgs& a, unsigned char* ws, cudaStream_t stream) {
+  // (one row's drafts have none before it)
+  return a.history || (a.draft && a.S > 1) || a.nbias > 0 ? launch_passes<T, kVector, true>(a, ws, stream)
+                                                          : launch_passes<T, kVector, false>(a, ws, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_probs(const ProbsArgs& a, cudaStream_t stream) {
-  probs_kernel<<<(unsigned)(a.B * a.S), kThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+size_t probs_workspace_bytes(int B, int S, int V, int history_cap, int nbias) {
+  return probs_layout(B, S, V, history_cap, nbias).total;
+}
+
+cudaError_t launch_probs(const ProbsArgs& a, void* workspace, cudaStream_t stream) {
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  const uintptr_t align = a.dtype == DSA_F32 ? 16 : 8;
+  const bool vector = a.V % 4 == 0 && reinterpret_cast<uintptr_t>(a.logits) % align == 0 &&
+                      reinterpret_cast<uintptr_t>(a.p) % 16 == 0;
+  if (a.dtype == DSA_F32) return vector ? launch<float, true>(a, ws, stream) : launch<float, false>(a, ws, stream);
+  return vector ? launch<__nv_bfloat16, true>(a, ws, stream) : launch<__nv_bfloat16, false>(a, ws, stream);
 }
 
 }  // namespace dsa

@@ -103,8 +103,9 @@ __global__ void __launch_bounds__(256) rope_wide_kernel(RopeArgs a, const __grid
     const int h = head0 + i * (int)blockDim.y;
     if (there && h < a.heads) {
       v0[i] = *reinterpret_cast<const uint4*>(x + h * a.x_head);
-      if constexpr (kHalf)
+      if constexpr (kHalf) {
         if (!pass) v1[i] = *reinterpret_cast<const uint4*>(x + h * a.x_head + e1);
+      }
     }
   }
   const int threads = blockDim.x * blockDim.y * blockDim.z;

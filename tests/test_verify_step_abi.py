@@ -119,8 +119,8 @@ def test_paged_attn_refusals(L):
 
 def test_logits_probs_refusals(L):
     names = ["logits", "dtype", "B", "S", "V", "temperature", "repetition", "frequency", "presence", "history", "cap",
-             "history_len", "prompt_len", "draft", "bias_ids", "bias_values", "nbias", "mask", "p"]
-    ok = dict(logits=FAKE, dtype=1, B=2, S=3, V=100, p=FAKE, cap=0, nbias=0)
+             "history_len", "prompt_len", "draft", "bias_ids", "bias_values", "nbias", "mask", "p", "ws", "size"]
+    ok = dict(logits=FAKE, dtype=1, B=2, S=3, V=100, p=FAKE, cap=0, nbias=0, ws=FAKE, size=1 << 30)
 
     def call(**kw):
         a = {**ok, **kw}
@@ -133,6 +133,17 @@ def test_logits_probs_refusals(L):
         assert call(**kw) == -1, kw
     assert call(dtype=2) == -2
     assert call(cap=1 << 30, history=FAKE) == -2
+    need = L.dsa_probs_workspace_size(2, 3, 100, 0, 0)
+    assert need > 0
+    for kw in [dict(ws=None), dict(size=need - 1), dict(ws=TWO)]:
+        assert call(**kw) == -3, kw
+    more = L.dsa_probs_workspace_size(2, 3, 100, 50, 4)
+    assert more > need
+    assert call(cap=50, history=FAKE, nbias=4, bias_ids=FAKE, bias_values=FAKE, size=more - 1) == -3
+    assert call(S=65536) == -2 and call(nbias=1 << 28, bias_ids=FAKE, bias_values=FAKE) == -2
+    for sizes in [(0, 1, 10, 0, 0), (1, 0, 10, 0, 0), (1, 1, 0, 0, 0), (1, 1, 1 << 24, 0, 0), (1 << 20, 1 << 20, 10, 0, 0),
+                  (1, 1, 10, -1, 0), (1, 1, 10, 0, -1), (1, 65536, 10, 0, 0), (1, 1, 10, 1 << 28, 0)]:
+        assert L.dsa_probs_workspace_size(*sizes) == 0
 
 
 def test_binding_refuses_cpu_tensors():
