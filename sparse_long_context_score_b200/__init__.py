@@ -446,49 +446,64 @@ def dsa_decode_step(groups, k: int, scale: float, ws=None, stream=None, side=Non
 
 
 # ---------------------------------------------------------------- around the verify step
-# These calls are short: a decode step's take a few microseconds on the GPU, so the checks
-# below are kept to one pass over each tensor.
-def _arg(t, dtypes, shape, name, dev):
-    """Address of a dense tensor on `dev` (None: a null pointer)."""
+# These calls are short -- a decode step's take a few microseconds on the GPU -- so a right
+# argument is checked in one expression, and what is wrong with a wrong one is looked for after.
+_dtypes = {}
+
+
+def _types():
+    """Tensor types by name, made once torch is there."""
+    if not _dtypes:
+        torch = _torch()
+        _dtypes.update(bf16=frozenset(_bf16_types()), f32=frozenset((torch.float32,)), i32=frozenset((torch.int32,)),
+                       i64=frozenset((torch.int64,)), u8=frozenset((torch.uint8,)),
+                       float=frozenset((torch.float32, torch.bfloat16)))
+    return _dtypes
+
+
+def _arg(t, kind, shape, name, dev):
+    """Address of a dense tensor on `dev` (None: a null pointer); shape None: any."""
     if t is None:
         return None
-    if not isinstance(t, _torch().Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
+    try:
+        if t.dtype in _dtypes[kind] and t.device == dev and (shape is None or t.shape == shape) and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}") from None
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
-    if t.shape != shape:
+    if t.dtype not in _dtypes[kind]:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {tuple(_dtypes[kind])}")
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _device(t, name):
     """The CUDA device of a tensor."""
-    if not isinstance(t, _torch().Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
-    return t.device
+    _types()
+    try:
+        if t.is_cuda:
+            return t.device
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}") from None
+    raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
 
 
-def _call(name, dev, stream, *args):
-    """The C call `name` with `dev` current, on `stream` (None: the current one of `dev`)."""
+def _call(fn, dev, stream, *args):
+    """The C call `fn` with `dev` current, on `stream` (None: the current one of `dev`)."""
     torch = _torch()
     if stream is None:
         raw = torch._C._cuda_getCurrentRawStream(dev.index)
     else:
         raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    fn = getattr(lib(), name)
     if dev.index == torch.cuda.current_device():
         rc = fn(*args, raw)
     else:
         with torch.cuda.device(dev):
             rc = fn(*args, raw)
-    if rc != DSA_OK:
-        _check(rc, name)
+    if rc:
+        _check(rc, fn.__name__)
 
 
 def dsa_rope_init(rot_dim: int, layout: str = "interleaved", theta: float = 10000.0, factor: float = 1.0,
@@ -520,24 +535,22 @@ def dsa_rope(x, positions, plan: RopePlan, rot_offset: int = 0, out=None, stream
     xs, os_ = x.stride(), out.stride()
     if out.shape != x.shape or (dim > 1 and (xs[2] != 1 or os_[2] != 1)):
         raise ValueError("out must have x's shape, and both a dense last dimension")
-    ptr = _arg(positions, (torch.int64,), (n,), "positions", dev)
+    ptr = _arg(positions, "i64", (n,), "positions", dev)
     if n and heads:
-        _call("dsa_rope", dev, stream, x.data_ptr(), ptr, n, heads, dim, int(rot_offset), ctypes.addressof(plan),
+        _call(lib().dsa_rope, dev, stream, x.data_ptr(), ptr, n, heads, dim, int(rot_offset), ctypes.addressof(plan),
               int(dtype == torch.float32), xs[0], xs[1], out.data_ptr(), os_[0], os_[1])
     return out
 
 
 def _paged(cache, table, cu_q, ctx_len, dev):
     """Checked pointers of a paged batch, its sequences, and the pool's sizes."""
-    torch = _torch()
-    i32 = (torch.int32,)
-    _device(cache, "cache"), _device(table, "table")
-    if cache.dim() != 3 or table.dim() != 2:
-        raise ValueError("cache must be [pages, page_size, 576] and table [B, max_pages]")
-    P, page, _ = cache.shape
-    B, most = table.shape
-    return (_arg(cache, _bf16_types(), (P, page, DQK), "cache", dev), _arg(table, i32, (B, most), "table", dev),
-            _arg(cu_q, i32, (B + 1,), "cu_q", dev), _arg(ctx_len, i32, (B,), "ctx_len", dev)), B, (P, page, most)
+    try:
+        P, page, width = cache.shape
+        B, most = table.shape
+    except (AttributeError, ValueError):
+        raise ValueError("cache must be a [pages, page_size, 576] and table a [B, max_pages] tensor") from None
+    return (_arg(cache, "bf16", (P, page, DQK), "cache", dev), _arg(table, "i32", None, "table", dev),
+            _arg(cu_q, "i32", (B + 1,), "cu_q", dev), _arg(ctx_len, "i32", (B,), "ctx_len", dev)), B, (P, page, most)
 
 
 def dsa_cache_append(x, gamma, eps: float, plan: RopePlan, cache, table, cu_q, ctx_len, stream=None):
@@ -545,13 +558,13 @@ def dsa_cache_append(x, gamma, eps: float, plan: RopePlan, cache, table, cu_q, c
     strided) to the pages of their sequences; gamma [512] bf16, cache [pages, page_size, 576]
     bf16, table [B, max_pages], cu_q [B+1] and ctx_len [B] int32.  Returns cache."""
     dev = _device(x, "x")
-    if x.dtype not in _bf16_types() or x.dim() != 2 or x.shape[1] != DQK or x.stride(1) != 1:
+    n, stride = x.shape[0], x.stride()
+    if x.dtype not in _dtypes["bf16"] or x.shape != (n, DQK) or stride[1] != 1:
         raise ValueError(f"x must be [n, {DQK}] bf16 with dense rows")
-    n = x.shape[0]
     ptrs, B, pages = _paged(cache, table, cu_q, ctx_len, dev)
-    gm = _arg(gamma, _bf16_types(), (DV,), "gamma", dev)
+    gm = _arg(gamma, "bf16", (DV,), "gamma", dev)
     if n:
-        _call("dsa_cache_append", dev, stream, x.data_ptr(), x.stride(0) if n > 1 else DQK, gm, float(eps),
+        _call(lib().dsa_cache_append, dev, stream, x.data_ptr(), stride[0] if n > 1 else DQK, gm, float(eps),
               ctypes.addressof(plan), *ptrs, n, B, *pages)
     return cache
 
@@ -580,13 +593,11 @@ def dsa_paged_attn(q, cache, table, cu_q, ctx_len, scale: float, out=None, lse=N
     ptrs, B, pages = _paged(cache, table, cu_q, ctx_len, dev)
     if ws is None:
         ws = paged_workspace(n, B, H, dev)
-    args = (_arg(q, _bf16_types(), (n, H, DQK), "q", dev), *ptrs, n, B, H, *pages, float(scale),
-            _arg(out, _bf16_types(), (n, H, DV), "out", dev), _arg(lse, (torch.float32,), (n, H), "lse", dev),
-            _ptr(ws, (torch.uint8,), "workspace"), ws.numel())
-    if ws.device != dev:
-        raise ValueError(f"workspace is on {ws.device}, expected {dev}")
+    args = (_arg(q, "bf16", (n, H, DQK), "q", dev), *ptrs, n, B, H, *pages, float(scale),
+            _arg(out, "bf16", (n, H, DV), "out", dev), _arg(lse, "f32", (n, H), "lse", dev),
+            _arg(ws, "u8", None, "workspace", dev), ws.numel())
     if n:
-        _call("dsa_paged_attn", dev, stream, *args)
+        _call(lib().dsa_paged_attn, dev, stream, *args)
     return out, lse
 
 
@@ -603,7 +614,7 @@ def dsa_logits_probs(logits, temperature=None, history=None, history_len=None, p
     B, S, V = logits.shape
     if out is None:
         out = torch.empty((B, S, V), dtype=torch.float32, device=dev)
-    f32, i32, row = (torch.float32,), (torch.int32,), (B,)
+    row = (B,)
     cap = nb = 0
     if history is not None:
         cap = history.shape[1]
@@ -613,18 +624,15 @@ def dsa_logits_probs(logits, temperature=None, history=None, history_len=None, p
         raise ValueError("bias_ids and bias_values go together")
     if bias_ids is not None:
         nb = bias_ids.shape[1]
-    args = (_arg(logits, (torch.float32, torch.bfloat16), (B, S, V), "logits", dev), int(logits.dtype == torch.float32),
-            B, S, V, _arg(temperature, f32, row, "temperature", dev), _arg(repetition, f32, row, "repetition", dev),
-            _arg(frequency, f32, row, "frequency", dev), _arg(presence, f32, row, "presence", dev),
-            _arg(history, i32, (B, cap), "history", dev), cap, _arg(history_len, i32, row, "history_len", dev),
-            _arg(prompt_len, i32, row, "prompt_len", dev), _arg(draft, i32, (B, S), "draft", dev),
-            _arg(bias_ids, i32, (B, nb), "bias_ids", dev), _arg(bias_values, f32, (B, nb), "bias_values", dev), nb,
-            _arg(mask, i32, (B, S, (V + 31) // 32), "mask", dev), _arg(out, f32, (B, S, V), "out", dev))
+    args = (_arg(logits, "float", (B, S, V), "logits", dev), int(logits.dtype == torch.float32), B, S, V,
+            _arg(temperature, "f32", row, "temperature", dev), _arg(repetition, "f32", row, "repetition", dev),
+            _arg(frequency, "f32", row, "frequency", dev), _arg(presence, "f32", row, "presence", dev),
+            _arg(history, "i32", (B, cap), "history", dev), cap, _arg(history_len, "i32", row, "history_len", dev),
+            _arg(prompt_len, "i32", row, "prompt_len", dev), _arg(draft, "i32", (B, S), "draft", dev),
+            _arg(bias_ids, "i32", (B, nb), "bias_ids", dev), _arg(bias_values, "f32", (B, nb), "bias_values", dev), nb,
+            _arg(mask, "i32", (B, S, (V + 31) // 32), "mask", dev), _arg(out, "f32", (B, S, V), "out", dev))
     if B and S:
         if ws is None:
             ws = torch.empty(lib().dsa_probs_workspace_size(B, S, V, cap, nb), dtype=torch.uint8, device=dev)
-        elif ws.device != dev:
-            raise ValueError(f"workspace is on {ws.device}, expected {dev}")
-        args += (_ptr(ws, (torch.uint8,), "workspace"), ws.numel())
-        _call("dsa_logits_probs", dev, stream, *args)
+        _call(lib().dsa_logits_probs, dev, stream, *args, _arg(ws, "u8", None, "workspace", dev), ws.numel())
     return out

@@ -849,9 +849,10 @@ cudaError_t launch_paged_attn(const uint16_t* q, const uint16_t* cache, const Pa
   while (box < kKeys && p.page_size % (2 * box) == 0) box *= 2;
   CUtensorMap qmap, cmap, rmap;
   const long long pool = (long long)p.num_pages * p.page_size;
-  if (!make_map_576(&qmap, q, (long long)p.n * H, kRows, kBlocks) || !make_map_576(&cmap, cache, pool, box, 2) ||
-      !make_map_576(&rmap, cache, pool, box, 1))
+  if (!make_map_576(&qmap, q, (long long)p.n * H, kRows, kBlocks) || !make_map_576(&rmap, cache, pool, box, 1))
     return cudaErrorInvalidValue;
+  cmap = rmap;  // (only whole tiles are copied two blocks at a time)
+  if (box == kKeys && !make_map_576(&cmap, cache, pool, box, 2)) return cudaErrorInvalidValue;
   const PagedLayout l = paged_layout(ctas);
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   Join* joins = reinterpret_cast<Join*>(ws + l.joins);

@@ -137,9 +137,9 @@ def test_logits_probs_refusals(L):
     assert need > 0
     for kw in [dict(ws=None), dict(size=need - 1), dict(ws=TWO)]:
         assert call(**kw) == -3, kw
-    more = L.dsa_probs_workspace_size(2, 3, 100, 50, 4)
+    more = L.dsa_probs_workspace_size(2, 3, 100, 5000, 4)
     assert more > need
-    assert call(cap=50, history=FAKE, nbias=4, bias_ids=FAKE, bias_values=FAKE, size=more - 1) == -3
+    assert call(cap=5000, history=FAKE, nbias=4, bias_ids=FAKE, bias_values=FAKE, size=more - 1) == -3
     assert call(S=65536) == -2 and call(nbias=1 << 28, bias_ids=FAKE, bias_values=FAKE) == -2
     for sizes in [(0, 1, 10, 0, 0), (1, 0, 10, 0, 0), (1, 1, 0, 0, 0), (1, 1, 1 << 24, 0, 0), (1 << 20, 1 << 20, 10, 0, 0),
                   (1, 1, 10, -1, 0), (1, 1, 10, 0, -1), (1, 65536, 10, 0, 0), (1, 1, 10, 1 << 28, 0)]:
