@@ -9,9 +9,15 @@
 // (query tile, key tile) pairs of the whole batch, in order, are dealt out in equal
 // contiguous shares, one a CTA and one CTA an SM: a long context is split over CTAs when
 // there are few query rows, and a CTA works through many query tiles when there are many.
-// The lengths are read on the device, and every CTA finds its own share.  A query tile that one CTA covers is written directly, the parts of one that crosses a
-// share's border go to the workspace in 32 bits and paged_combine_kernel joins them in the
-// CTAs' order (no atomics: the result does not depend on timing).
+// The lengths are read on the device, and every CTA finds its own share.  A query tile that one
+// CTA covers is written directly; the parts of one that crosses a share's border go to the
+// workspace in 32 bits, and paged_combine_kernel joins them in the CTAs' order (no atomics: the
+// result does not depend on timing).
+// Query tiles of one sequence meet its rows in L2 only where their CTAs read the same ones at
+// about the same time, and the shares' borders shift from tile to tile.  So every CTA starts where
+// its key tile's number is a multiple of the share's length, and takes the ones before that
+// last: at any time the CTAs of a sequence are at the same few places (16 sequences of 2 to 8 new
+// tokens x 64 heads over 4K to 32K: 1.29 -> 0.73 GB from HBM, 371 -> 351 us).
 //
 // One key tile of a CTA, everything in shared memory beside the 64 query rows (73.7 KB):
 //   S^T = K Q^T     M = 128 keys, N = 64 rows, K = 576        (36 MMAs; TMEM lane = key)
@@ -51,7 +57,7 @@ constexpr int kLoadWarp = 0, kMmaWarp = 1, kQueryWarp = 2, kWalkWarp = 3, kSoftm
 constexpr int kSoftmaxThreads = 256;             // eight warps: two per TMEM lane quarter
 constexpr int kThreadsP = kSoftmaxWarp0 * 32 + kSoftmaxThreads;  // 384
 constexpr float kRescaleLog2 = 8.f;
-constexpr int kPrefetchTiles = 4;
+constexpr int kPrefetchTiles = 64;
 
 // One CTA's part of a query tile.
 struct Segment {
@@ -59,12 +65,19 @@ struct Segment {
   int row0;      // first query row (token * H + head) in q
   int nrows;     // rows of the tile that exist
   int tile_row;  // the same row, counted from the sequence's first
-  int k0, k1;    // key tiles
+  int k0, k1;    // key tiles, visited from `turn` on: k0 + turn .. k1 - 1, then k0 ..
+  int turn;
   int seen0;     // cached rows that the sequence's first new token sees
   int limit;     // cached rows of the sequence
   int tiles;     // query tiles of the sequence
   int part;      // workspace slot of this part of the tile; -1: the tile is whole
 };
+
+// The i-th key tile that a segment visits.
+__device__ __forceinline__ int tile_at(const Segment& s, int i) {
+  const int k = s.k0 + s.turn + i;
+  return k < s.k1 ? k : k - (s.k1 - s.k0);
+}
 
 // Where a CTA's share starts: key tile k0 of query tile `tile` of sequence b (-1: nowhere),
 // and its key tiles.
@@ -327,6 +340,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
           s.tiles = w.tiles;
           s.part = k0 > 0 ? 2 * cta : s.k1 < keys ? 2 * cta + 1 : -1;
           if (k0 == 0 && s.k1 < keys) join = Join{s.row0, s.nrows, 1 + (keys - s.k1 + first.keys - 1) / first.keys, 0};
+          const int next_phase = (k0 + first.keys - 1) / first.keys * first.keys;  // a multiple of the share
+          s.turn = next_phase < s.k1 ? next_phase - k0 : 0;
           left -= s.k1 - k0;
           k0 = 0;
           ++tile;
@@ -362,19 +377,21 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
     bool ok = true;
     while (ok && next_segment(s)) {
       const int32_t* table = p.table + (size_t)s.b * p.max_pages;
-      auto page_row = [&](int k) {  // pool row of this lane's box in key tile k, -1 where there is none
-        if (lane >= boxes || k >= s.k1) return -1;
-        const long long pos = (long long)kKeys * k + box * lane;
+      const int count = s.k1 - s.k0;
+      auto page_row = [&](int n) {  // pool row of this lane's box in the n-th key tile, -1 where there is none
+        if (lane >= boxes || n >= count) return -1;
+        const long long pos = (long long)kKeys * tile_at(s, n) + box * lane;
         const long long i = pos / p.page_size;
         if (i >= p.max_pages) return -1;
         const int page = table[i];
         return page >= 0 && page < p.num_pages ? page * p.page_size + (int)(pos - i * p.page_size) : -1;
       };
-      int row = page_row(s.k0), next = page_row(s.k0 + 1);
-      // A context that few query tiles read comes from HBM: its tiles are brought into L2 two
-      // ahead, so that the stream goes on while the blocks of shared memory are in use.  (By
-      // plain prefetches: the copy engine takes as long for a prefetched tile as for a loaded
-      // one.)
+      int row = page_row(0), next = page_row(1);
+      // A context that few query tiles read comes mostly from HBM: its tiles are brought into L2
+      // two ahead, so that the stream goes on while the blocks of shared memory are in use (2 to 8
+      // tokens x 64 heads: 354 -> 338 us; one token: HBM is busy either way; a prefill chunk's 512
+      // tiles: 1% slower).  By plain prefetches: the copy engine takes as long for a prefetched
+      // tile as for a loaded one.
       const bool from_hbm = s.tiles <= kPrefetchTiles;
       auto prefetch = [&](int r) {
         if (!from_hbm) return;
@@ -388,8 +405,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
         }
       };
       prefetch(next);
-      for (int k = s.k0; k < s.k1; ++k, ++it) {
-        const int ahead = page_row(k + 2);
+      for (int n = 0; n < count; ++n, ++it) {
+        const int ahead = page_row(n + 2);
         const uint32_t there = __ballot_sync(0xFFFFFFFFu, row >= 0);
         uint32_t bad = 0;  // per 16 rows
         for (int i = 0; i < kKeys / 16; ++i) bad |= ((there >> (i * 16 / box)) & 1u ? 0u : 1u) << i;
@@ -440,7 +457,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
     bool ok = true;
     for (int i = 0; ok && next_segment(s); ++i) {
       ok = warp_wait(qfull_bar, i & 1, 45);
-      for (int k = s.k0; ok && k < s.k1; ++k, ++it) {
+      const int count = s.k1 - s.k0;
+      for (int n = 0; ok && n < count; ++n, ++it) {
         // (unrolled, so that descriptors are a base and a constant: an issue loop that adds
         // them up at run time is slower than the tensor core)
 #pragma unroll
@@ -459,14 +477,14 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
         if (!ok) break;
         if (leader) {
           mma_commit(sfull_bar);
-          if (k + 1 == s.k1) mma_commit(qfree_bar);
+          if (n + 1 == count) mma_commit(qfree_bar);
         }
         __syncwarp();
         // the epilogue of the segment before has read O
-        if (k == s.k0) ok = warp_wait(ofree_bar, (i & 1) ^ 1, 47);
+        if (n == 0) ok = warp_wait(ofree_bar, (i & 1) ^ 1, 47);
         ok = ok && warp_wait(pfull_bar, pp++ & 1, 48);
         if (!ok) break;
-        if (k > s.k0 && k + 1 < s.k1 && *s_over == (uint32_t)it + 1u) {  // a wrong guess: the tile's weights again
+        if (n > 0 && n + 1 < count && *s_over == (uint32_t)it + 1u) {  // a wrong guess: the tile's weights again
           __syncwarp();
           if (lane == 0) mbar_arrive(sfull_bar);
           ok = warp_wait(pfull_bar, pp++ & 1, 57);
@@ -480,11 +498,11 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
             for (int ks = 0; ks < kKeys / 16; ++ks)
               mma_bf16(tmem + kTmemO + 64 * mb, dv + (uint64_t)((2 * mb * kBlockBytes + ks * 16 * 128) >> 4),
                        dp + (uint64_t)(ks * 16 * 128 >> 4), idPV,
-                       k > s.k0 || ks > 0 ? 1u : 0u);
+                       n > 0 || ks > 0 ? 1u : 0u);
             mma_commit(free_bar(mb));
           }
           mma_commit(free_bar(4));
-          if (k + 1 == s.k1) mma_commit(ofull_bar);
+          if (n + 1 == count) mma_commit(ofull_bar);
         }
         __syncwarp();
       }
@@ -527,7 +545,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
         l[r] = 0.f;
       }
       bool guessed = false;
-      for (int next = s.k0; next < s.k1;) {
+      const int count = s.k1 - s.k0;
+      for (int next = 0; next < count;) {
         ok = warp_wait(sfull_bar, sp & 1, 51);
         if (!ok) break;
         ++sp;
@@ -537,8 +556,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
         // tile again (S is still there), which then goes through the exchange of maxima as a
         // segment's first and last tiles do.
         const bool redo = guessed && *s_over == tiles;
-        const int k = redo ? next - 1 : next;
-        const bool exchange = redo || k == s.k0 || k + 1 == s.k1;
+        const int n = redo ? next - 1 : next, k = tile_at(s, n);
+        const bool exchange = redo || n == 0 || n + 1 == count;
         if (!redo) ++tiles;
         const uint32_t bad = *s_bad;
         uint32_t z[32];
@@ -593,7 +612,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
             m[r] = __shfl_sync(0xFFFFFFFFu, mrow, r);
             l[r] *= __shfl_sync(0xFFFFFFFFu, alpha, r);
           }
-          if (k > s.k0) {
+          if (n > 0) {
             if (quarter == 0) {
               s_alpha[32 * half + lane] = alpha;
               if (lane == 0) s_vote[half] = scaled ? 1u : 0u;
@@ -647,7 +666,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
         __syncwarp();
         if (lane == 0) mbar_arrive(pfull_bar);
         guessed = !exchange;
-        next = k + 1;
+        next = n + 1;
       }
       if (!ok) break;
       // sums over the warp's keys, row 32 half + lane to each lane: at step o the rows whose
