@@ -117,6 +117,9 @@ constexpr int kTmemCols = 512;
 constexpr int kPartFloats = kRows * kDv;             // one part's [64][512] sums
 
 constexpr float kRescaleFactor = 256.f;  // 2^kRescaleLog2
+// The maximum that weights are taken from before a row has one: a logit of minus infinity weighs
+// nothing (from -inf it would be NaN), any other one too much, so that a guess is taken back.
+constexpr float kNoMax = -3e38f;
 
 // 2^x; results below the normal range become zero
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -138,6 +141,14 @@ __device__ __forceinline__ float min_nan(float x, float y) {  // NaN if x is
 // natural logarithm of 2^m sum; -inf for an empty sum
 __device__ __forceinline__ float log_sum(float m, float sum) {
   return sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.69314718055994531f;
+}
+// eight bf16 values, NaN and infinity made zero
+__device__ __forceinline__ uint4 finite_bf16(uint4 x) {
+  auto two = [](uint32_t w) {
+    if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
+    return (w & 0x7F800000u) == 0x7F800000u ? w & 0xFFFFu : w;
+  };
+  return make_uint4(two(x.x), two(x.y), two(x.z), two(x.w));
 }
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
@@ -536,12 +547,13 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
     uint32_t tiles = 0;  // key tiles weighted, this CTA's first being number 1
     bool ok = true;
     for (int i = 0; ok && next_segment(s); ++i) {
-      const int seen_first = min(s.seen0 + s.tile_row / H, s.limit);  // rows that all 64 see
+      // cached rows that all of the tile's query rows see, and those that some do
+      const int seen_first = min(s.seen0 + s.tile_row / H, s.limit);
+      const int seen_last = min(s.seen0 + (s.tile_row + s.nrows - 1) / H, s.limit);
       float m[32], l[32];
       float mrow = 32 * half + lane < s.nrows ? -INFINITY : INFINITY;  // row 32 half + lane's maximum
 #pragma unroll
       for (int r = 0; r < 32; ++r) {
-        m[r] = 32 * half + r < s.nrows ? -INFINITY : INFINITY;  // (a row that is none weighs nothing)
         l[r] = 0.f;
       }
       bool guessed = false;
@@ -609,7 +621,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
           const bool scaled = __any_sync(0xFFFFFFFFu, alpha != 1.f);
 #pragma unroll
           for (int r = 0; r < 32; ++r) {
-            m[r] = __shfl_sync(0xFFFFFFFFu, mrow, r);
+            m[r] = fmaxf(__shfl_sync(0xFFFFFFFFu, mrow, r), kNoMax);
             l[r] *= __shfl_sync(0xFFFFFFFFu, alpha, r);
           }
           if (n > 0) {
@@ -653,12 +665,16 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                        pack_bf16x2(p[4], p[5]), pack_bf16x2(p[6], p[7]));
         }
         if (!exchange && __any_sync(0xFFFFFFFFu, most > kRescaleFactor) && lane == 0) *s_over = tiles;
-        if (bad != 0 || kKeys * (k + 1) > s.limit) {
-          // rows that are no cached rows may hold anything, NaN included: as values they are zero
-          for (int x = st; x < kKeys * 64; x += kSoftmaxThreads) {  // (row, 16-byte chunk of 8 blocks)
+        if (!whole) {
+          // A weight of zero does not silence a value of NaN or infinity.  Rows that no query row
+          // of the tile sees may hold anything: as values they are zero.  Of a row that some see,
+          // only such entries become zero: S has them, so where the row is seen they count.
+          const int first = bad != 0 ? 0 : max(0, seen_first - kKeys * k);
+          for (int x = 64 * first + st; x < kKeys * 64; x += kSoftmaxThreads) {  // (row, 16-byte chunk of 8 blocks)
             const int row = x >> 6, blk = (x >> 3) & 7, ch = x & 7;
-            if (kKeys * k + row >= s.limit || ((bad >> (row >> 4)) & 1u))
-              *reinterpret_cast<uint4*>(smem + kOffStage + blk * kBlockBytes + row * 128 + ch * 16) = make_uint4(0, 0, 0, 0);
+            uint4* at = reinterpret_cast<uint4*>(smem + kOffStage + blk * kBlockBytes + row * 128 + ch * 16);
+            if (kKeys * k + row >= seen_last || ((bad >> (row >> 4)) & 1u)) *at = make_uint4(0, 0, 0, 0);
+            else if (kKeys * k + row >= seen_first) *at = finite_bf16(*at);
           }
         }
         fence_proxy_async();  // P (and the zeros) are visible to the tensor core

@@ -82,6 +82,122 @@ def test_sharp_flat_and_growing_logits(dsa, std, order):
     _check(dsa.dsa_paged_attn(q, batch.cache, batch.table, batch.cu_q, batch.ctx_len, 0.0), batch, q, 0.0)
 
 
+def _long_batch(growing, seed):
+    """48 sequences of 4 new tokens over some 20 key tiles each: a CTA's share is a few whole
+    query tiles, so most key tiles lie in the middle of one."""
+    batch = Batch([4] * 48, [2300 + 17 * i for i in range(48)], 64, seed=seed).fill(seed=seed)
+    flat = batch.cache.view(-1, DQK)
+    for b in range(48):
+        r = batch.rows(b).cuda()
+        steps = torch.linspace(0.02, 1.0, len(r), device="cuda") if growing else torch.linspace(1.0, 0.02, len(r), device="cuda")
+        flat[r] = (flat[r].float() * steps[:, None]).to(torch.bfloat16)
+    return batch
+
+
+@pytest.mark.parametrize("growing", [True, False])
+def test_the_maximum_moves_in_the_middle_of_a_long_row(dsa, growing):
+    batch = _long_batch(growing, 11)
+    q = _queries(batch.n, 64, std=8.0)
+    for scale in (SCALE, -SCALE):
+        _check(dsa.dsa_paged_attn(q, batch.cache, batch.table, batch.cu_q, batch.ctx_len, scale), batch, q, scale)
+
+
+def test_single_keys_far_above_the_rest(dsa):
+    """One row's logit jumps by 2^30 and more at one key, or at key after key of one tile, while the
+    63 rows beside it go on as they were."""
+    batch = _long_batch(False, 12)
+    q = _queries(batch.n, 64)
+    flat = batch.cache.view(-1, DQK)
+    for b in range(48):
+        r = batch.rows(b)
+        for i, s in enumerate((700, 701, 1003, 1500 + b, 2000)):
+            t, h = batch.ends[b] + i % 4, (7 * b + 13 * i) % 64
+            flat[r[s]] = (q[t, h].float() * (1 + i)).to(torch.bfloat16)
+    _check(dsa.dsa_paged_attn(q, batch.cache, batch.table, batch.cu_q, batch.ctx_len, SCALE), batch, q)
+
+
+def test_rows_that_see_their_first_key_late(dsa):
+    """The pages at the start of every context are missing, whole key tiles of them."""
+    batch = _long_batch(False, 13)
+    for b in range(48):
+        batch.table[b, :3 + b % 24] = -1
+    q = _queries(batch.n, 64)
+    _check(dsa.dsa_paged_attn(q, batch.cache, batch.table, batch.cu_q, batch.ctx_len, SCALE), batch, q)
+
+
+@pytest.mark.parametrize("heads,new,ctx", [(64, 4, 300), (16, 7, 385), (1, 66, 66), (128, 3, 127)])
+@pytest.mark.parametrize("what", [math.nan, math.inf])
+def test_what_a_token_does_not_see_may_hold_anything(dsa, heads, new, ctx, what):
+    """The last new token's cached row is NaN or infinite: that token's business alone."""
+    batch = Batch([new, new], [ctx, 40 + new], 16, seed=heads).fill()
+    flat = batch.cache.view(-1, DQK)
+    for b in range(2):
+        flat[batch.rows(b)[-1]] = what
+    q = _queries(batch.n, heads)
+    out, lse = dsa.dsa_paged_attn(q, batch.cache, batch.table, batch.cu_q, batch.ctx_len, SCALE)
+    last = torch.tensor([new - 1, 2 * new - 1], device="cuda")
+    assert bool(lse[last].isnan().all()) and bool(out[last].isnan().all())
+    keep = torch.ones(batch.n, dtype=torch.bool, device="cuda")
+    keep[last] = False
+    ref = attention(batch, q, SCALE)
+    b_out, b_lse = attention_bounds(*ref, ctx)
+    assert bool(((out.double() - ref[0]).abs() <= b_out)[keep].all())
+    assert bool(((lse.double() - ref[1]).abs() <= b_lse)[keep].all())
+
+
+def test_a_bad_query_row_is_its_own_business(dsa):
+    batch = Batch([3, 2], [2000, 90], 64).fill()
+    q = _queries(batch.n, 64)
+    q[1, 5, 17], q[4, 63, 570] = math.nan, math.inf
+    out, lse = dsa.dsa_paged_attn(q, batch.cache, batch.table, batch.cu_q, batch.ctx_len, SCALE)
+    bad = torch.zeros((batch.n, 64), dtype=torch.bool, device="cuda")
+    bad[1, 5] = bad[4, 63] = True
+    assert bool(out[bad].isnan().all()) and bool(lse[bad].isnan().all())
+    ref = attention(batch, q, SCALE)
+    b_out, b_lse = attention_bounds(*ref, 2000)
+    assert bool(((out.double() - ref[0]).abs() <= b_out)[~bad].all())
+    assert bool(((lse.double() - ref[1]).abs() <= b_lse)[~bad].all())
+
+
+def test_logits_of_minus_infinity_weigh_nothing(dsa):
+    """Infinite rotary entries, as a mask would make them: those keys' logits are -inf, first ones,
+    whole tiles and last ones among them."""
+    batch = _long_batch(False, 14)
+    q = _queries(batch.n, 64)
+    q[..., DV] = 1.0
+    flat = batch.cache.view(-1, DQK)
+    for b in range(48):
+        r = batch.rows(b)
+        at = torch.cat((torch.arange(100 + 5 * b), torch.arange(900, 1400), torch.arange(len(r) - 3, len(r))))
+        flat[r[at], DV] = -math.inf
+    got = dsa.dsa_paged_attn(q, batch.cache, batch.table, batch.cu_q, batch.ctx_len, SCALE)
+    _check(got, batch, q)
+
+
+def test_more_sequences_than_threads_of_a_block(dsa):
+    new = [(0, 1, 2, 1)[i % 4] for i in range(1000)]
+    ctx = [(37 * i) % 400 + 2 for i in range(1000)]
+    batch = Batch(new, ctx, 16, seed=2).fill()
+    q = _queries(batch.n, 24)
+    _check(dsa.dsa_paged_attn(q, batch.cache, batch.table, batch.cu_q, batch.ctx_len, SCALE), batch, q)
+
+
+def test_two_calls_at_once(dsa):
+    """Two streams, two workspaces: neither call sees the other's parts."""
+    jobs = []
+    for i, (new, ctx) in enumerate([([2, 1], [9000, 3000]), ([1, 3, 1], [700, 12000, 5000])]):
+        batch = Batch(new, ctx, 64, seed=i).fill(seed=i)
+        q = _queries(batch.n, 64, seed=i)
+        out, lse = torch.empty((batch.n, 64, DV), dtype=torch.bfloat16, device="cuda"), torch.empty((batch.n, 64), device="cuda")
+        jobs.append((batch, q, out, lse, dsa.paged_workspace(batch.n, len(new), 64), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for batch, q, out, lse, ws, stream in jobs:
+            dsa.dsa_paged_attn(q, batch.cache, batch.table, batch.cu_q, batch.ctx_len, SCALE, out=out, lse=lse, ws=ws, stream=stream)
+    torch.cuda.synchronize()
+    for batch, q, out, lse, _, _ in jobs:
+        _check((out, lse), batch, q)
+
 @pytest.mark.parametrize("heads", [16, 64])
 def test_tokens_that_see_nothing_and_rows_that_are_not_there(dsa, heads):
     # sequence 0 has more new tokens than cached ones: its first three see nothing
