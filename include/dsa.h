@@ -441,9 +441,11 @@ dsa_status dsa_cache_append(const uint16_t *x, long long x_stride, const uint16_
  *   lse  [n, H] f32 out:         ln sum_s exp(scale * q . c[s]) (-inf when none); may be NULL
  * bf16 operands (the weights are rounded to bf16 before the product with the values), f32
  * accumulation and softmax, one rounding of the output.  Rows behind ctx_len[b] may hold
- * anything, NaN included; the rows of a sequence's cached tokens must be finite.
+ * anything, NaN included, and a cached row that is not finite concerns only the tokens that see
+ * it: a logit of NaN or +inf makes a token's row of out and lse NaN, one of -inf weighs nothing.
  * workspace: dsa_paged_workspace_size(n, B, H) bytes, 256-byte aligned, written by every call
  * (calls that overlap on the GPU need one each); the size depends on the current device.
+ * out and lse must not overlap an input or each other.
  */
 size_t dsa_paged_workspace_size(int n, int B, int H);
 dsa_status dsa_paged_attn(const uint16_t *q, const uint16_t *cache, const int32_t *table, const int32_t *cu_q,
@@ -476,7 +478,7 @@ dsa_status dsa_paged_attn(const uint16_t *q, const uint16_t *cache, const int32_
  * Ids outside [0, V) are skipped (padding).  p must not overlap an input.
  * workspace: dsa_probs_workspace_size bytes (history_cap 0 without a history), 256-byte aligned,
  * written by every call (calls that overlap on the GPU need one each).  S <= 65535,
- * nbias < 2^28.
+ * nbias <= 4096 (biases are few: one on much of the vocabulary belongs in the logits).
  */
 size_t dsa_probs_workspace_size(int B, int S, int V, int history_cap, int nbias);
 dsa_status dsa_logits_probs(const void *logits, int dtype, int B, int S, int V, const float *temperature,

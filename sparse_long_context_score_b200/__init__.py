@@ -506,6 +506,15 @@ def _call(fn, dev, stream, *args):
         _check(rc, fn.__name__)
 
 
+def _room(stream, dev):
+    """Where tensors that a call on `stream` makes for itself come from: that stream's memory, so
+    that neither what another stream still does with a block nor what it does next can meet it."""
+    torch = _torch()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), dev) if int(stream) else torch.cuda.default_stream(dev)
+    return torch.cuda.stream(stream)
+
+
 def dsa_rope_init(rot_dim: int, layout: str = "interleaved", theta: float = 10000.0, factor: float = 1.0,
                   orig_len: int = 0) -> RopePlan:
     """The plan of a rotary embedding (see include/dsa.h): `layout` "half" or "interleaved";
@@ -524,6 +533,9 @@ def dsa_rope(x, positions, plan: RopePlan, rot_offset: int = 0, out=None, stream
     rotated, the others copied.  `out` may be x (in place) or a strided tensor apart from it."""
     torch = _torch()
     dev = _device(x, "x")
+    if stream is not None and out is None:
+        with _room(stream, dev):
+            return dsa_rope(x, positions, plan, rot_offset)
     n, heads, dim = x.shape
     if out is None:
         out = torch.empty((n, heads, dim), dtype=x.dtype, device=dev)
@@ -585,6 +597,9 @@ def dsa_paged_attn(q, cache, table, cu_q, ctx_len, scale: float, out=None, lse=N
     cache (see dsa_cache_append) -> (out [n, H, 512] bf16, lse [n, H] f32)."""
     torch = _torch()
     dev = _device(q, "q")
+    if stream is not None and (out is None or lse is None or ws is None):
+        with _room(stream, dev):
+            return dsa_paged_attn(q, cache, table, cu_q, ctx_len, scale, out, lse, ws)
     n, H, _ = q.shape
     if out is None:
         out = torch.empty((n, H, DV), dtype=torch.bfloat16, device=dev)
@@ -611,6 +626,10 @@ def dsa_logits_probs(logits, temperature=None, history=None, history_len=None, p
     at temperature [B] (0: one-hot at the maximum)."""
     torch = _torch()
     dev = _device(logits, "logits")
+    if stream is not None and (out is None or ws is None):
+        with _room(stream, dev):
+            return dsa_logits_probs(logits, temperature, history, history_len, prompt_len, draft, repetition, frequency,
+                                    presence, bias_ids, bias_values, mask, out, ws)
     B, S, V = logits.shape
     if out is None:
         out = torch.empty((B, S, V), dtype=torch.float32, device=dev)

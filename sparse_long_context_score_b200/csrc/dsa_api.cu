@@ -42,6 +42,12 @@ namespace {
 
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// Whether two ranges of memory share a byte.
+inline bool overlap(const void* p, size_t p_bytes, const void* q, size_t q_bytes) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return a < b ? b - a < p_bytes : a - b < q_bytes;
+}
+
 inline size_t round256(size_t b) { return (b + 255) & ~(size_t)255; }
 
 bool sizes_ok(int B, int T, int N) {
@@ -579,6 +585,8 @@ dsa_status dsa_cache_append(const uint16_t* x, long long x_stride, const uint16_
     return DSA_ERR_INVALID_ARG;
   if (plan->rot_dim != kDqk - kDv) return DSA_ERR_UNSUPPORTED;
   if (n == 0) return DSA_OK;
+  const size_t pool = (size_t)num_pages * page_size * kDqk * 2;
+  if (overlap(cache, pool, x, ((size_t)(n - 1) * x_stride + kDqk) * 2)) return DSA_ERR_INVALID_ARG;
   const PagedBatch pb{table, cu_q, ctx_len, n, B, max_pages, num_pages, page_size};
   return cuda_status(launch_cache_append(x, x_stride, gamma, eps, *plan, pb, cache, stream));
 }
@@ -598,6 +606,11 @@ dsa_status dsa_paged_attn(const uint16_t* q, const uint16_t* cache, const int32_
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4)) return DSA_ERR_INVALID_ARG;
   if (H > 128 || (long long)n * H > 0x7FFFFFFFLL) return DSA_ERR_UNSUPPORTED;
   if (n == 0) return DSA_OK;
+  const size_t rows = (size_t)n * H, pool = (size_t)num_pages * page_size * kDqk * 2;
+  if (overlap(out, rows * kDv * 2, q, rows * kDqk * 2) || overlap(out, rows * kDv * 2, cache, pool) ||
+      (lse && (overlap(lse, rows * 4, q, rows * kDqk * 2) || overlap(lse, rows * 4, cache, pool) ||
+               overlap(lse, rows * 4, out, rows * kDv * 2))))
+    return DSA_ERR_INVALID_ARG;
   const size_t need = paged_attn_workspace_bytes();
   if (need == 0) return cuda_status(cudaErrorInvalidDevice);
   if (!workspace || workspace_bytes < need || !aligned(workspace, 256)) return DSA_ERR_WORKSPACE;
@@ -607,7 +620,7 @@ dsa_status dsa_paged_attn(const uint16_t* q, const uint16_t* cache, const int32_
 
 size_t dsa_probs_workspace_size(int B, int S, int V, int history_cap, int nbias) {
   if (B <= 0 || S <= 0 || S > 65535 || V <= 0 || V >= (1 << 24) || (long long)B * S > 0x7FFFFFFFLL || history_cap < 0 ||
-      history_cap >= (1 << 28) || nbias < 0 || nbias >= (1 << 28))
+      history_cap >= (1 << 28) || nbias < 0 || nbias > 4096)
     return 0;
   return probs_workspace_bytes(B, S, V, history_cap, nbias);
 }
@@ -622,7 +635,7 @@ dsa_status dsa_logits_probs(const void* logits, int dtype, int B, int S, int V, 
       (long long)B * S > 0x7FFFFFFFLL || (nbias > 0 && (!bias_ids || !bias_values)))
     return DSA_ERR_INVALID_ARG;
   if (dtype != DSA_BF16 && dtype != DSA_F32) return DSA_ERR_UNSUPPORTED;
-  if (history_cap >= (1 << 28) || nbias >= (1 << 28) || S > 65535) return DSA_ERR_UNSUPPORTED;
+  if (history_cap >= (1 << 28) || nbias > 4096 || S > 65535) return DSA_ERR_UNSUPPORTED;
   if (!aligned(logits, dtype == DSA_F32 ? 4 : 2)) return DSA_ERR_INVALID_ARG;
   const void* words[] = {p,       temperature, repetition, frequency, presence,    history,
                          history_len, prompt_len,  draft,      bias_ids,  bias_values, mask};
@@ -652,6 +665,8 @@ dsa_status dsa_logits_probs(const void* logits, int dtype, int B, int S, int V, 
   if (!workspace || workspace_bytes < probs_workspace_bytes(B, S, V, history ? history_cap : 0, nbias) ||
       !aligned(workspace, 256))
     return DSA_ERR_WORKSPACE;
+  const size_t entries = (size_t)B * S * V;
+  if (overlap(p, entries * 4, logits, entries * (dtype == DSA_F32 ? 4 : 2))) return DSA_ERR_INVALID_ARG;
   return cuda_status(launch_probs(a, workspace, stream));
 }
 

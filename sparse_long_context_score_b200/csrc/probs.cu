@@ -262,7 +262,8 @@ __global__ void __launch_bounds__(kThreads) probs_listed_kernel(const __grid_con
   const int j0 = blockIdx.z * kListedRows, rows = min(a.S - j0, kListedRows);
   const size_t row0 = (size_t)b * a.S + j0;
   // The second of these kernels starts when all CTAs of the second pass are past their wait, which
-  // the lists and the partials are complete behind: it waits for that pass only where it writes.
+  // the lists and the partials are complete behind: it waits for that pass only before it writes,
+  // or ends (what comes behind it in the stream takes the pass for done, too).
   if (!kWrite) {
     sm100::grid_dep_wait();
     sm100::grid_dep_launch();
@@ -319,7 +320,9 @@ __global__ void __launch_bounds__(kThreads) probs_listed_kernel(const __grid_con
       for (int i = 0; i < kListedRows; ++i)
         if (there && i < rows) a.p[(row0 + i) * V + v] = z[i];
     }
-  } else if (!kWrite && threadIdx.x < kListedRows * kWarps) {  // nothing but gaps
+  } else if constexpr (kWrite) {  // nothing but gaps
+    sm100::grid_dep_wait();
+  } else if (threadIdx.x < kListedRows * kWarps) {
     s_part[threadIdx.x / kWarps][threadIdx.x % kWarps] = Partial{-INFINITY, set.greedy ? kNoPlace : 0.f};
   }
   if constexpr (!kWrite) {

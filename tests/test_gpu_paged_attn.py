@@ -281,6 +281,13 @@ def test_another_stream(dsa):
     dsa.dsa_paged_attn(q, batch.cache, batch.table, batch.cu_q, batch.ctx_len, SCALE, out=out, lse=lse, ws=ws, stream=side)
     side.synchronize()
     _check((out, lse), batch, q)
+    # a block that the current stream has freed and still writes is none of that stream's
+    torch.cuda._sleep(20_000_000)
+    blocks = [torch.empty_like(t).fill_(3) for t in (out, lse, ws)]
+    del blocks
+    got = dsa.dsa_paged_attn(q, batch.cache, batch.table, batch.cu_q, batch.ctx_len, SCALE, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], out) and torch.equal(got[1], lse)
 
 
 def test_offsets_past_32_bits(dsa):

@@ -24,20 +24,21 @@ def _gen(seed):
     return g
 
 
-def _inputs(B, S, V, seed=0, dtype=torch.float32, hist=0, bias=0, mask=False, greedy=()):
+def _inputs(B, S, V, seed=0, dtype=torch.float32, hist=0, bias=0, mask=False, greedy=(), spread=False):
     g = _gen(seed)
     u = lambda lo, hi: lo + (hi - lo) * torch.rand(B, generator=g, device="cuda")  # noqa: E731
     a = dict(logits=(torch.randn((B, S, V), generator=g, device="cuda") * 3).to(dtype), temperature=u(0.4, 1.5))
     for b in greedy:
         a["temperature"][b] = 0.0
+    ids = V if spread else 300  # (a history's tokens: many times the same, or anywhere)
     if hist:
-        a["history"] = torch.randint(-2, min(V + 2, 300), (B, hist), generator=g, device="cuda", dtype=torch.int32)
+        a["history"] = torch.randint(-2, min(V + 2, ids), (B, hist), generator=g, device="cuda", dtype=torch.int32)
         a["history_len"] = torch.randint(0, hist + 5, (B,), generator=g, device="cuda", dtype=torch.int32)
         a["prompt_len"] = torch.randint(0, hist, (B,), generator=g, device="cuda", dtype=torch.int32)
-        a["draft"] = torch.randint(-1, min(V + 1, 300), (B, S), generator=g, device="cuda", dtype=torch.int32)
+        a["draft"] = torch.randint(-1, min(V + 1, ids), (B, S), generator=g, device="cuda", dtype=torch.int32)
         a["repetition"], a["frequency"], a["presence"] = u(0.8, 1.4), u(-0.3, 0.6), u(-0.3, 0.6)
     if bias:
-        a["bias_ids"] = torch.randint(-1, min(V + 1, 2 * bias), (B, bias), generator=g, device="cuda", dtype=torch.int32)
+        a["bias_ids"] = torch.randint(-1, V + 1 if spread else min(V + 1, 2 * bias), (B, bias), generator=g, device="cuda", dtype=torch.int32)
         a["bias_values"] = torch.randn((B, bias), generator=g, device="cuda") * 3
     if mask:
         a["mask"] = torch.randint(-(1 << 31), 1 << 31, (B, S, (V + 31) // 32), generator=g, device="cuda").to(torch.int32)
@@ -70,23 +71,48 @@ def _check(dsa, a):
     (2, 2, 1000, dict(hist=200, bias=20, mask=True, greedy=(0,))), (1, 4, 4097, dict(hist=50)),
     (5, 1, 20480, dict(bias=5)), (2, 1, 32003, dict(mask=True)), (1, 7, 50257, dict(hist=3000, bias=100, mask=True)),
     (2, 2, 151552, dict(hist=1000, bias=8, mask=True, greedy=(1,))), (1, 2, 163841, dict(hist=100)),
-    (1, 1, 262144, dict(mask=True, hist=10)), (1, 1, 327681, {}), (1, 1, 700001, dict(hist=64, bias=4, mask=True))])
+    (1, 1, 262144, dict(mask=True, hist=10)), (1, 1, 327681, {}), (1, 1, 700001, dict(hist=64, bias=4, mask=True)),
+    # many rows: two passes over chunks
+    (300, 1, 1, {}), (70, 5, 31, dict(hist=20, bias=5, mask=True, greedy=(3, 69))), (320, 1, 64, dict(hist=1)),
+    (100, 3, 1000, dict(hist=700, spread=True)), (40, 4, 5003, dict(hist=300, bias=40, mask=True, greedy=(0, 7))),
+    (16, 7, 20480, dict(hist=6000, bias=32, mask=True, spread=True, greedy=(5,))), (50, 4, 4096, dict(bias=300, spread=True)),
+    (30, 5, 8193, dict(hist=40, bias=1, spread=True)), (2, 90, 12289, dict(hist=500, mask=True, spread=True))])
 def test_matches_its_definition(dsa, dtype, B, S, V, kw):
     _check(dsa, _inputs(B, S, V, seed=V, dtype=dtype, **kw))
 
 
-def test_each_step_alone(dsa):
-    full = _inputs(3, 4, 5003, seed=1, hist=400, bias=30, mask=True, greedy=(2,))
+@pytest.mark.parametrize("B", [3, 50])
+def test_each_step_alone(dsa, B):
+    full = _inputs(B, 4, 5003, seed=1, hist=400, bias=30, mask=True, greedy=(2,))
     for keep in [(), ("history",), ("draft",), ("history", "repetition"), ("history", "history_len", "frequency"),
                  ("history", "prompt_len", "presence"), ("draft", "repetition", "presence"), ("draft", "frequency"),
                  ("bias_ids", "bias_values"), ("mask",), ("temperature",), ("repetition", "frequency", "presence")]:
         _check(dsa, {"logits": full["logits"], **{k: full[k] for k in keep}})
 
 
-def test_counts_are_exact(dsa):
+def test_vocabularies_beyond_the_second_level_cache(dsa):
+    """145 MB of logits, taken in groups of sequences; the last one is smaller."""
+    _check(dsa, _inputs(37, 3, 325001, seed=3, hist=100, bias=3, spread=True, greedy=(36,)))
+
+
+def test_very_many_short_rows(dsa):
+    """A CTA takes all 80 rows of a sequence."""
+    z = torch.randn((600, 80, 64), generator=_gen(6), device="cuda") * 4
+    T = 0.5 + torch.rand(600, generator=_gen(7), device="cuda")
+    want = torch.softmax(z.double() / T.double()[:, None, None], -1)
+    assert bool(((dsa.dsa_logits_probs(z, T).double() - want).abs() <= 2.0 ** -14 * want + 1e-37).all())
+    history = torch.full((600, 3), 9, dtype=torch.int32, device="cuda")
+    got = dsa.dsa_logits_probs(z, T, history=history, frequency=torch.full((600,), 0.5, device="cuda"))
+    z[..., 9] -= 1.5
+    want = torch.softmax(z.double() / T.double()[:, None, None], -1)
+    assert bool(((got.double() - want).abs() <= 2.0 ** -14 * want + 1e-37).all())
+
+
+@pytest.mark.parametrize("V", [3000, 400000])
+def test_counts_are_exact(dsa, V):
     """One token said thousands of times, one in the prompt alone, one only drafted; the same
     bias twice: values exact in 32 bits."""
-    V, L = 3000, 5000
+    L = 5000
     z = torch.zeros((1, 3, V), device="cuda")
     z[..., 17], z[..., 18], z[..., 19], z[..., 20] = 2000.0, 8.0, -4.0, 5.0
     history = torch.full((1, L), 17, dtype=torch.int32, device="cuda")
@@ -169,21 +195,61 @@ def test_unaligned_rows_outputs_and_repeats(dsa):
             assert torch.equal(dsa.dsa_logits_probs(z), out)
 
 
-def test_a_captured_call_reads_the_present_history(dsa):
-    a = _inputs(2, 3, 60000, seed=5, hist=500, bias=10, mask=True)
-    out = torch.zeros((2, 3, 60000), device="cuda")
+@pytest.mark.parametrize("B,V", [(2, 60000), (20, 60000), (1, 400000)])
+def test_a_captured_call_reads_the_present_history(dsa, B, V):
+    a = _inputs(B, 3, V, seed=5, hist=500, bias=10, mask=True)
+    out = torch.zeros((B, 3, V), device="cuda")
     dsa.dsa_logits_probs(**a, out=out)
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         dsa.dsa_logits_probs(**a, out=out)
     for seed in (6, 7):
-        b = _inputs(2, 3, 60000, seed=seed, hist=500, bias=10, mask=True)
+        b = _inputs(B, 3, V, seed=seed, hist=500, bias=10, mask=True)
         for k in a:
             a[k].copy_(b[k])
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, dsa.dsa_logits_probs(**b))
+
+
+@pytest.mark.parametrize("B,V", [(3, 30000), (20, 60001)])
+def test_two_calls_at_once_and_lists_that_name_nothing(dsa, B, V):
+    """Two streams with a workspace each; one call's history, drafts and biases are all padding."""
+    jobs = []
+    for seed in (1, 2):
+        a = _inputs(B, 4, V, seed=seed, hist=300, bias=6, mask=seed == 1)
+        if seed == 2:
+            for name in ("history", "draft", "bias_ids"):
+                a[name].fill_(-1)
+        jobs.append((a, torch.full((B, 4, V), 7.0, device="cuda"), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for a, out, stream in jobs:
+            dsa.dsa_logits_probs(**a, out=out, stream=stream)
+    torch.cuda.synchronize()
+    for a, out, _ in jobs:
+        assert torch.equal(out, dsa.dsa_logits_probs(**a))
+    _check(dsa, jobs[0][0])
+    _check(dsa, jobs[1][0])
+
+
+def test_results_of_another_stream_keep_to_themselves(dsa):
+    """What a call on another stream makes for itself is not a block that the current stream has
+    freed and still writes."""
+    stream = torch.cuda.Stream()
+    z = torch.randn((4, 5, 50000), generator=_gen(8), device="cuda")
+    want = dsa.dsa_logits_probs(z)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)  # (some 10 ms)
+    block = torch.empty_like(want).fill_(3.0)
+    del block
+    got = dsa.dsa_logits_probs(z, stream=stream)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    again = dsa.dsa_logits_probs(z, stream=stream.cuda_stream)
+    torch.cuda.synchronize()
+    assert torch.equal(again, want)
 
 
 def test_binding_refusals(dsa):
@@ -197,6 +263,12 @@ def test_binding_refusals(dsa):
             dsa.dsa_logits_probs(z, **kw)
     with pytest.raises(TypeError):
         dsa.dsa_logits_probs(z.half())
+    with pytest.raises(dsa.DsaError) as err:
+        dsa.dsa_logits_probs(z, out=z)
+    assert err.value.status == -1
+    with pytest.raises(dsa.DsaError) as err:
+        dsa.dsa_logits_probs(z, bias_ids=ints(2, 5000), bias_values=torch.zeros((2, 5000), device="cuda"))
+    assert err.value.status == -2
     assert dsa.dsa_logits_probs(z[:0]).shape == (0, 1, 64)
 
 

@@ -202,3 +202,66 @@ def test_append_over_many_sequences(dsa):
     want = y / (y.pow(2).mean(-1, keepdim=True) + 1e-6).sqrt()
     assert bool(((flat[where.cuda(), :DV].double() - want).abs() <= (2.0 ** -8 + 2.0 ** -17) * want.abs()).all())
     assert int((flat != 0).any(-1).sum()) == batch.n
+
+
+def test_captured_calls_follow_positions_lengths_and_tables(dsa):
+    """A graph on a side stream: queries rotated in place, rows appended; replayed with other
+    positions, sequences and pages, on a padded batch."""
+    n, H, plan = 9, 8, dsa.dsa_rope_init(64)
+    q = torch.zeros((n, H, DQK), dtype=torch.bfloat16, device="cuda")
+    x = torch.zeros((n, DQK), dtype=torch.bfloat16, device="cuda")
+    positions = torch.zeros(n, dtype=torch.int64, device="cuda")
+    gamma = torch.ones(DV, device="cuda", dtype=torch.bfloat16)
+    cache = torch.zeros((64, 16, DQK), dtype=torch.bfloat16, device="cuda")
+    table = torch.zeros((3, 40), dtype=torch.int32, device="cuda")
+    cu_q, ctx_len = torch.zeros(4, dtype=torch.int32, device="cuda"), torch.zeros(3, dtype=torch.int32, device="cuda")
+
+    def step():
+        dsa.dsa_rope(q[..., DV:], positions, plan, out=q[..., DV:])
+        dsa.dsa_cache_append(x, gamma, 1e-6, plan, cache, table, cu_q, ctx_len)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i, (new, ctx) in enumerate([([1, 1, 1], [5, 300, 16]), ([3, 0, 2], [8, 0, 18]), ([0, 9, 0], [0, 9, 0])]):
+        batch = Batch(new, ctx, 16, seed=i)
+        g = _gen(i)
+        raw = torch.randn((n, H, DQK), generator=g, device="cuda").to(torch.bfloat16)
+        q.copy_(raw)
+        x.normal_(generator=g)
+        positions.copy_(torch.randint(0, 1 << 20, (n,), generator=g, device="cuda"))
+        cache.normal_(generator=g)
+        table.fill_(-1)
+        table[:, :batch.table.shape[1]] = batch.table
+        cu_q.copy_(batch.cu_q)
+        ctx_len.copy_(batch.ctx_len)
+        before = cache.clone()
+        graph.replay()
+        torch.cuda.synchronize()
+        _check_rope(raw, q, positions, DV, 64, "interleaved")
+        rows, want, bound = _append_reference(batch, x, gamma, 1e-6, *frequencies(64, 1e4), "interleaved")
+        flat = cache.view(-1, DQK)
+        assert len(rows) == sum(new) and bool(((flat[rows].double() - want).abs() <= bound).all())
+        rest = torch.ones(len(flat), dtype=torch.bool, device="cuda")
+        rest[rows] = False
+        assert torch.equal(flat[rest], before.view(-1, DQK)[rest])
+
+
+def test_a_rotation_on_another_stream_keeps_its_result(dsa):
+    """Its output is not a block that the current stream has freed and still writes."""
+    x = torch.randn((500, 16, 64), generator=_gen(7), device="cuda")
+    positions = torch.arange(500, device="cuda")
+    plan, side = dsa.dsa_rope_init(64), torch.cuda.Stream()
+    want = dsa.dsa_rope(x, positions, plan)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)  # (some 10 ms)
+    block = torch.empty_like(want).fill_(3.0)
+    del block
+    got = dsa.dsa_rope(x, positions, plan, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)

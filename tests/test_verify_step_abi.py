@@ -9,6 +9,7 @@ import sparse_long_context_score_b200 as dsa
 from verify_step import frequencies
 
 FAKE = ctypes.c_void_p(1 << 20)  # aligned, never dereferenced: every call below fails validation
+AT = 1 << 20
 ODD = ctypes.c_void_p((1 << 20) + 1)
 TWO = ctypes.c_void_p((1 << 20) + 2)
 
@@ -92,6 +93,7 @@ def test_append_refusals(L):
                dict(stride=577), dict(stride=580), dict(x=TWO), dict(gamma=TWO), dict(cache=TWO), dict(table=TWO),
                dict(eps=-1.0), dict(eps=math.nan)]:
         assert call(**kw) == -1, kw
+    assert call() == -1 and call(x=AT + 8 * 64 * 1152 - 16) == -1 and call(x=AT - 4 * 1152 + 16) == -1  # x in the cache
     assert call(page=24) == -2
     assert call(P=1 << 26, page=64) == -2
     assert call(plan=ctypes.addressof(wide)) == -2
@@ -111,6 +113,10 @@ def test_paged_attn_refusals(L):
                dict(B=0), dict(H=0), dict(P=0), dict(page=0), dict(most=0), dict(q=TWO), dict(cache=TWO), dict(out=TWO),
                dict(lse=TWO), dict(ctx=TWO), dict(scale=math.nan), dict(scale=math.inf)]:
         assert call(**kw) == -1, kw
+    apart = dict(q=FAKE, out=AT + (1 << 20), lse=AT + (1 << 21), cache=AT + (1 << 22))
+    for kw in [dict(out=FAKE), dict(out=AT + 4 * 16 * 1152 - 16), dict(out=AT + (1 << 22) + 1152), dict(lse=AT + 16),
+               dict(lse=AT + (1 << 20) + 64), dict(lse=AT + (1 << 22))]:  # outputs over inputs or one another
+        assert call(**{**apart, **kw}) == -1, kw
     for kw in [dict(H=129), dict(page=40), dict(P=1 << 26), dict(n=1 << 30)]:
         assert call(**kw) == -2, kw
     for n, B, H in [(-1, 1, 1), (1, 0, 1), (1, 1, 0), (1, 1, 129), (1 << 30, 1, 16)]:
@@ -140,9 +146,10 @@ def test_logits_probs_refusals(L):
     more = L.dsa_probs_workspace_size(2, 3, 100, 5000, 4)
     assert more > need
     assert call(cap=5000, history=FAKE, nbias=4, bias_ids=FAKE, bias_values=FAKE, size=more - 1) == -3
-    assert call(S=65536) == -2 and call(nbias=1 << 28, bias_ids=FAKE, bias_values=FAKE) == -2
+    assert call() == -1 and call(p=AT + 600 * 4 - 4) == -1 and call(p=AT + 600 * 2 - 4, dtype=0) == -1  # p over the logits
+    assert call(S=65536) == -2 and call(nbias=4097, bias_ids=FAKE, bias_values=FAKE) == -2
     for sizes in [(0, 1, 10, 0, 0), (1, 0, 10, 0, 0), (1, 1, 0, 0, 0), (1, 1, 1 << 24, 0, 0), (1 << 20, 1 << 20, 10, 0, 0),
-                  (1, 1, 10, -1, 0), (1, 1, 10, 0, -1), (1, 65536, 10, 0, 0), (1, 1, 10, 1 << 28, 0)]:
+                  (1, 1, 10, -1, 0), (1, 1, 10, 0, -1), (1, 65536, 10, 0, 0), (1, 1, 10, 1 << 28, 0), (1, 1, 10, 0, 4097)]:
         assert L.dsa_probs_workspace_size(*sizes) == 0
 
 
