@@ -6,8 +6,8 @@
 //
 // A sequence's query rows (token, head) are one matrix [n_b H, 576], cut into tiles of 64
 // rows whatever H is; a tile visits the 128-row key tiles that its last token sees.  The
-// (query tile, key tile) pairs of the whole batch, in order, are dealt out in equal
-// contiguous shares, one a CTA and one CTA an SM: a long context is split over CTAs when
+// (query tile, key tile) pairs of the whole batch, in order, are dealt out in contiguous
+// shares of equal work, one a CTA and one CTA an SM: a long context is split over CTAs when
 // there are few query rows, and a CTA works through many query tiles when there are many.
 // The lengths are read on the device, and every CTA finds its own share.  A query tile that one
 // CTA covers is written directly; the parts of one that crosses a share's border go to the
@@ -25,6 +25,9 @@
 // The tile (147.5 KB) fills the rest of shared memory as nine blocks of 64 columns, and
 // there is no second one: S takes the blocks as they arrive, and each quarter of PV gives
 // two of them back, so the next tile's loads run behind PV and the next S behind the loads.
+// What bounds it: 512 query tokens x 64 heads x 2 over 16K take 5.32K cycles a key tile, 27.7
+// bytes a cycle into each SM of the 29.5 that all SMs at once get out of L2 (S 1.73K and PV 1.54K
+// cycles of MMAs, the softmax 1.32K).  8 tokens over 128K each: 7.0K cycles a key tile, HBM.
 // Keys on the M side: an MMA of M = 128, N = 64, K = 16 takes 48 cycles (its operands'
 // 6 KB at 128 bytes a cycle); with the rows there, M = 64, N = 128 takes 64.
 #include <cudaTypedefs.h>
@@ -58,6 +61,11 @@ constexpr int kSoftmaxThreads = 256;             // eight warps: two per TMEM la
 constexpr int kThreadsP = kSoftmaxWarp0 * 32 + kSoftmaxThreads;  // 384
 constexpr float kRescaleLog2 = 8.f;
 constexpr int kPrefetchTiles = 64;
+// Beginning a query tile costs a CTA as much as so many key tiles: the end of the one before
+// (maxima, sums, 131 KB of values) and a first key tile that nothing runs ahead of take 10K cycles
+// more than the 5.4K of a key tile.  Shares of equal key tiles: 16 verify chunks 340 us instead of
+// 330, 8 x 128K 251 instead of 248 (a prefill chunk 2730 instead of 2737).
+constexpr int kTileCost = 2;
 
 // One CTA's part of a query tile.
 struct Segment {
@@ -79,10 +87,9 @@ __device__ __forceinline__ int tile_at(const Segment& s, int i) {
   return k < s.k1 ? k : k - (s.k1 - s.k0);
 }
 
-// Where a CTA's share starts: key tile k0 of query tile `tile` of sequence b (-1: nowhere),
-// and its key tiles.
+// A CTA's share: it starts `at` into query tile `tile` of sequence b (-1: nowhere).
 struct Share {
-  int b, tile, k0, keys;
+  int b, tile, at, length;
 };
 // A query tile that CTA g begins and later CTAs go on with, for the combine.
 struct Join {
@@ -174,16 +181,16 @@ __device__ __forceinline__ int tile_keys(const SequenceWork& w, int tile, int H)
   const int seen = min(w.seen0 + last / H, w.limit);
   return max(1, (seen + kKeys - 1) / kKeys);
 }
-// Key tiles that the query tiles before `tile` visit.  Tiles see ever more rows, so each key
+// Key tiles that the query tiles before `tile` visit, and what beginning them costs.  Tiles see ever more rows, so each key
 // tile m is visited from one query tile on: the first whose last row, of token
 // (64 (i + 1) - 1) / H, sees more than 128 m rows.
-__device__ __forceinline__ long long keys_before(const SequenceWork& w, int tile, int H) {
+__device__ __forceinline__ long long work_before(const SequenceWork& w, int tile, int H) {
   if (tile <= 0) return 0;
-  long long sum = 0;
+  long long sum = (long long)kTileCost * tile;
   const int whole = min(tile, w.tiles - 1);  // all but the last tile have 64 rows
   if (whole > 0) {
     const int first = tile_keys(w, 0, H), last = tile_keys(w, whole - 1, H);
-    sum = (long long)whole * first;
+    sum += (long long)whole * first;
     for (int m = first; m < last; ++m) {
       const long long token = (long long)kKeys * m + 1 - w.seen0;  // the first that sees key tile m
       const long long i = max(0LL, (token * H + kRows) / kRows - 1);  // (64 (i + 1) - 1) / H >= token
@@ -246,18 +253,18 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
     tmem_alloc(smem_u32(s_tmem), kTmemCols);
     tmem_relinquish();
   }
-  // Where this CTA's share starts: every CTA sums the batch's key tiles, a thread a sequence.
+  // Where this CTA's share starts: every CTA sums the batch's work, a thread a sequence.
   // (A launch of its own for that, read by all CTAs, took 6 us more at 8 sequences.)
   {
     long long* s_sum = reinterpret_cast<long long*>(smem + kOffSum);
     long long total = 0, own = 0, before = 0;
     SequenceWork w{0, 0, 0, 0};
-    auto scan = [&](int b0) {  // keys of sequence b0 + threadIdx.x, the sum before it, the sum of all 384
+    auto scan = [&](int b0) {  // work of sequence b0 + threadIdx.x, the sum before it, the sum of all 384
       const int b = b0 + threadIdx.x;
       own = 0;
       if (b < p.B) {
         w = sequence_work(p, b, H);
-        own = keys_before(w, w.tiles, H);
+        own = work_before(w, w.tiles, H);
       }
       long long v = own;
 #pragma unroll
@@ -287,13 +294,13 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
       else __syncthreads();
       const long long at = start - base - before;
       if (at >= 0 && at < own) {
-        int lo = 0, hi = w.tiles - 1;  // the last tile with keys_before <= at
+        int lo = 0, hi = w.tiles - 1;  // the last tile that starts at or before it
         while (lo < hi) {
           const int mid = (lo + hi + 1) / 2;
-          if (keys_before(w, mid, H) <= at) lo = mid;
+          if (work_before(w, mid, H) <= at) lo = mid;
           else hi = mid - 1;
         }
-        *s_share = Share{b0 + (int)threadIdx.x, lo, (int)(at - keys_before(w, lo, H)), (int)min(per, 0x7FFFFFFFLL)};
+        *s_share = Share{b0 + (int)threadIdx.x, lo, (int)(at - work_before(w, lo, H)), (int)min(per, 0x7FFFFFFFLL)};
       }
       base += all;
     }
@@ -326,7 +333,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
       tma_prefetch(&cmap);
       tma_prefetch(&rmap);
       const Share first = *s_share;
-      int left = first.keys, b = first.b, tile = first.tile, k0 = first.k0;
+      int b = first.b, tile = first.tile, k0 = max(0, first.at - kTileCost);
+      int left = first.length - max(0, kTileCost - first.at);
       Join join{0, 0, 0, 0};
       SequenceWork w{0, 0, 0, 0};
       if (b >= 0) w = sequence_work(p, b, H);
@@ -350,10 +358,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
           s.limit = w.limit;
           s.tiles = w.tiles;
           s.part = k0 > 0 ? 2 * cta : s.k1 < keys ? 2 * cta + 1 : -1;
-          if (k0 == 0 && s.k1 < keys) join = Join{s.row0, s.nrows, 1 + (keys - s.k1 + first.keys - 1) / first.keys, 0};
-          const int next_phase = (k0 + first.keys - 1) / first.keys * first.keys;  // a multiple of the share
+          if (k0 == 0 && s.k1 < keys) join = Join{s.row0, s.nrows, 1 + (keys - s.k1 + first.length - 1) / first.length, 0};
+          const int next_phase = (k0 + first.length - 1) / first.length * first.length;  // a multiple of the share
           s.turn = next_phase < s.k1 ? next_phase - k0 : 0;
-          left -= s.k1 - k0;
+          left -= s.k1 - k0 + kTileCost;
           k0 = 0;
           ++tile;
         }
