@@ -722,7 +722,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
 #pragma unroll 1
       for (int mb = 2 * half; mb < 2 * half + 2; ++mb)
 #pragma unroll 1
-        for (int c0 = 0; c0 < 64; c0 += 32) {
+        for (int c0 = 0; c0 < s.nrows; c0 += 32) {
           uint32_t o[32];
           tmem_ld32(tmem + lane_addr + kTmemO + 64 * mb + c0, o);
           tmem_ld_wait();
