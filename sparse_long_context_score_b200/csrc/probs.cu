@@ -208,13 +208,14 @@ __device__ __forceinline__ void note_tokens(const ProbsArgs& a, int b, int v0, i
 // The shared memory that gathers a chunk's listed entries.
 struct Gathered {
   uint32_t words[kChunk];  // by entry
-  int number, names, below;  // listed entries; names in the chunk, and in those before
+  int number[kWarps];      // listed entries of the warps' threads
+  int names, below;        // names in the chunk, and in those before
 };
 // s_bias: by entry, where biases are given
 __device__ __forceinline__ void gather(const ProbsArgs& a, int b, int v0, int v1, Gathered& g, float* s_bias) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   for (int i = tid; i < kChunk / 4; i += kThreads) reinterpret_cast<uint4*>(g.words)[i] = make_uint4(0, 0, 0, 0);
-  if (tid == 0) g.number = g.names = g.below = 0;
+  if (tid == 0) g.names = g.below = 0;
   __syncthreads();
   int below = 0, names = 0;
   note_tokens(a, b, v0, v1, 0, g.words, names, below);
@@ -365,15 +366,30 @@ __global__ void __launch_bounds__(kThreads, kBlocks) probs_kernel(const __grid_c
     for (int i = 0; i < kItems; ++i) listed |= (g.words[place<kVector>(i)] != 0u ? 1u : 0u) << i;
     if (blockIdx.z == 0) {
       Listed* out = lists.entries + (size_t)b * lists.room + g.below;
-      int at = listed ? atomicAdd(&g.number, __popc(listed)) : 0;  // (the order within a chunk does not matter)
+      // by thread, not as they come: the order decides how the row's sum is rounded
+      const int own = __popc(listed);
+      int at = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xFFFFFFFFu, at, o);
+        if (lane >= o) at += u;
+      }
+      if (lane == 31) g.number[warp] = at;
+      at -= own;
+      __syncthreads();
+      int number = 0;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) at += g.number[w];
+        number += g.number[w];
+      }
       for (uint32_t todo = listed; todo; todo &= todo - 1) {
         const uint32_t e = place<kVector>(__ffs(todo) - 1), word = g.words[e];
         out[at++] = {(v0 + e) | (word & (kSeen | kBiased)), word & kCount, word & kBiased ? s_bias[e] : 0.f};
       }
-      __syncthreads();
       // gaps: behind this chunk's entries, and behind the last chunk's
       const int end = chunk == (int)gridDim.x - 1 ? lists.room - g.below : g.names;
-      for (int i = g.number + threadIdx.x; i < end; i += kThreads) out[i].v = kNobody;
+      for (int i = number + threadIdx.x; i < end; i += kThreads) out[i].v = kNobody;
     }
   }
   // the mask's bits of a row, by entry, without the listed entries; loaded a row ahead

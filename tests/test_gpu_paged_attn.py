@@ -99,7 +99,11 @@ def test_the_maximum_moves_in_the_middle_of_a_long_row(dsa, growing):
     batch = _long_batch(growing, 11)
     q = _queries(batch.n, 64, std=8.0)
     for scale in (SCALE, -SCALE):
-        _check(dsa.dsa_paged_attn(q, batch.cache, batch.table, batch.cu_q, batch.ctx_len, scale), batch, q, scale)
+        got = dsa.dsa_paged_attn(q, batch.cache, batch.table, batch.cu_q, batch.ctx_len, scale)
+        _check(got, batch, q, scale)
+        for _ in range(5):
+            again = dsa.dsa_paged_attn(q, batch.cache, batch.table, batch.cu_q, batch.ctx_len, scale)
+            assert torch.equal(again[0], got[0]) and torch.equal(again[1], got[1])
 
 
 def test_single_keys_far_above_the_rest(dsa):

@@ -213,6 +213,14 @@ def test_a_captured_call_reads_the_present_history(dsa, B, V):
         assert torch.equal(out, dsa.dsa_logits_probs(**b))
 
 
+@pytest.mark.parametrize("B,V", [(2, 30000), (24, 60000), (1, 700000)])
+def test_repeats_bit_for_bit(dsa, B, V):
+    a = _inputs(B, 4, V, seed=11, hist=3000, bias=40, mask=True, spread=True)
+    first = dsa.dsa_logits_probs(**a)
+    for _ in range(30):
+        assert torch.equal(dsa.dsa_logits_probs(**a), first)
+
+
 @pytest.mark.parametrize("B,V", [(3, 30000), (20, 60001)])
 def test_two_calls_at_once_and_lists_that_name_nothing(dsa, B, V):
     """Two streams with a workspace each; one call's history, drafts and biases are all padding."""
