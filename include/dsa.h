@@ -417,7 +417,8 @@ dsa_status dsa_rope(const void *x, const long long *positions, long long n, int 
  *   ctx_len  [B] i32
  * The lengths and the table are read on the device, so a captured call follows them.  A
  * position that the table does not hold (behind max_pages, or whose entry is not in
- * [0, num_pages)) is not there: it is not written, and no query sees it.
+ * [0, num_pages)) is not there: it is not written, and no query sees it.  The attention sees
+ * positions below 2^31 - 256.
  *
  * dsa_cache_append writes the new tokens' rows:
  *   x      [n, 576] bf16, row stride x_stride (a multiple of 8 elements): 512 latent and 64

@@ -510,8 +510,9 @@ def _room(stream, dev):
     """Where tensors that a call on `stream` makes for itself come from: that stream's memory, so
     that neither what another stream still does with a block nor what it does next can meet it."""
     torch = _torch()
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), dev) if int(stream) else torch.cuda.default_stream(dev)
+    if not isinstance(stream, torch.cuda.Stream):
+        raw = int(getattr(stream, "cuda_stream", stream))
+        stream = torch.cuda.ExternalStream(raw, dev) if raw else torch.cuda.default_stream(dev)
     return torch.cuda.stream(stream)
 
 

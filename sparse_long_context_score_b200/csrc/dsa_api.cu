@@ -600,7 +600,7 @@ dsa_status dsa_paged_attn(const uint16_t* q, const uint16_t* cache, const int32_
                           const int32_t* ctx_len, int n, int B, int H, int num_pages, int page_size, int max_pages,
                           float scale, uint16_t* out, float* lse, void* workspace, size_t workspace_bytes,
                           cudaStream_t stream) {
-  if (!q || !out || H <= 0 || !std::isfinite(scale)) return DSA_ERR_INVALID_ARG;
+  if (!q || !out || H <= 0 || !std::isfinite(scale * 1.4426950408889634f)) return DSA_ERR_INVALID_ARG;
   const dsa_status st = check_paged(cache, table, cu_q, ctx_len, n, B, num_pages, page_size, max_pages);
   if (st != DSA_OK) return st;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4)) return DSA_ERR_INVALID_ARG;

@@ -170,7 +170,8 @@ __device__ __forceinline__ SequenceWork sequence_work(const PagedBatch& p, int b
   SequenceWork w;
   w.rows = q0 < 0 ? 0 : max(min(q1, p.n) - q0, 0) * H;
   w.tiles = (w.rows + kRows - 1) / kRows;
-  w.limit = (int)max(0LL, min((long long)p.ctx_len[b], (long long)p.max_pages * p.page_size));
+  // (below 2^31 by two key tiles, so that a tile's end stays an int)
+  w.limit = (int)max(0LL, min(min((long long)p.ctx_len[b], 0x7FFFFF00LL), (long long)p.max_pages * p.page_size));
   w.seen0 = p.ctx_len[b] - (q1 - q0) + 1;
   return w;
 }
@@ -759,7 +760,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
 // The parts are CTA g's last and the first of the CTAs behind it.  Four warps take a row, 128
 // value dims each, with eight parts' loads in flight beside those of their (m, l); the (tile,
 // row) pairs of all joins are spread over the whole grid, since a few long contexts leave few
-// tiles of many parts, and many short ones the other way round.
+// tiles of many parts, and many short ones the other way round.  (16 verify chunks: some 220
+// parts, 29 MB; 14 us with cold caches.)
 constexpr int kJoinThreads = 256, kJoinRows = kJoinThreads / 128, kJoinBlocks = 3;  // blocks per SM
 __global__ void __launch_bounds__(kJoinThreads, kJoinBlocks)
 paged_combine_kernel(int ctas, const Join* joins, const float* parts, const float2* part_ml, uint16_t* out, float* lse) {

@@ -203,7 +203,8 @@ __device__ __forceinline__ int find_sequence(const PagedBatch& p, int token, int
 // One warp per token: lane l holds latent entries 8 l .. 8 l + 7 and 256 + 8 l .. 256 + 8 l + 7
 // and the angle of rotary pair l; lanes 0 .. 7 hold the rotary part's eight chunks and take the
 // angles (in the half layout also the other ends) from the lanes that have them.  The row is
-// loaded before its place is looked up.
+// loaded before its place is looked up.  16 chunks of up to 8 tokens take 2.6 us, 10.9K tokens 7.8 us
+// (3.2 TB/s): the chain of loads from the lengths over the table to the row's place.
 constexpr int kAppendWarps = 4;
 __global__ void __launch_bounds__(32 * kAppendWarps) append_kernel(const uint16_t* __restrict__ x, long long x_stride,
                                                                    const uint16_t* __restrict__ gamma, float eps,

@@ -294,6 +294,35 @@ def test_another_stream(dsa):
     assert torch.equal(got[0], out) and torch.equal(got[1], lse)
 
 
+def test_without_lse_and_on_the_default_stream(dsa):
+    batch = Batch([2, 1], [3000, 90], 64).fill()
+    q = _queries(3, 64)
+    out = torch.empty((3, 64, DV), dtype=torch.bfloat16, device="cuda")
+    ws = dsa.paged_workspace(3, 2, 64)
+    rc = dsa.lib().dsa_paged_attn(q.data_ptr(), batch.cache.data_ptr(), batch.table.data_ptr(), batch.cu_q.data_ptr(),
+                                  batch.ctx_len.data_ptr(), 3, 2, 64, batch.P, 64, batch.table.shape[1], SCALE, out.data_ptr(),
+                                  None, ws.data_ptr(), ws.numel(), None)
+    assert rc == 0
+    torch.cuda.synchronize()
+    got = dsa.dsa_paged_attn(q, batch.cache, batch.table, batch.cu_q, batch.ctx_len, SCALE, stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], out)
+
+
+def test_a_length_of_2_to_31(dsa):
+    """One page again and again behind a context of 2^31 - 1: the new token's position is past what
+    a table row holds, so it sees the table's 2^20 rows."""
+    batch = Batch([1], [16], 16).fill()
+    table = batch.table[:, :1].expand(1, 1 << 16).contiguous()
+    ctx = torch.tensor([(1 << 31) - 1], dtype=torch.int32, device="cuda")
+    q = _queries(1, 16)
+    out, lse = dsa.dsa_paged_attn(q, batch.cache, table, batch.cu_q, ctx, SCALE)
+    want, want_lse, size, reach = attention(batch, q, SCALE)
+    b_out, b_lse = attention_bounds(want, want_lse, size, reach, 1 << 20)
+    assert bool(((out.double() - want).abs() <= b_out).all())
+    assert bool(((lse.double() - want_lse - math.log(1 << 16)).abs() <= b_lse).all())
+
+
 def test_offsets_past_32_bits(dsa):
     """A pool of 5 GB: the last pages start behind 2^32 bytes."""
     batch = Batch([1], [400], 64)

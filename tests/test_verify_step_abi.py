@@ -111,7 +111,7 @@ def test_paged_attn_refusals(L):
     assert call(n=0) == 0
     for kw in [dict(q=None), dict(cache=None), dict(table=None), dict(cu=None), dict(ctx=None), dict(out=None), dict(n=-1),
                dict(B=0), dict(H=0), dict(P=0), dict(page=0), dict(most=0), dict(q=TWO), dict(cache=TWO), dict(out=TWO),
-               dict(lse=TWO), dict(ctx=TWO), dict(scale=math.nan), dict(scale=math.inf)]:
+               dict(lse=TWO), dict(ctx=TWO), dict(scale=math.nan), dict(scale=math.inf), dict(scale=-3e38)]:
         assert call(**kw) == -1, kw
     apart = dict(q=FAKE, out=AT + (1 << 20), lse=AT + (1 << 21), cache=AT + (1 << 22))
     for kw in [dict(out=FAKE), dict(out=AT + 4 * 16 * 1152 - 16), dict(out=AT + (1 << 22) + 1152), dict(lse=AT + 16),
