@@ -45,6 +45,12 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // One pair of a chunk or a row: the largest logit and the sum of exp((z - m) / T) -- where the
 // temperature asks for the maximum alone, the lowest index at it.
 struct Partial {
@@ -63,9 +69,7 @@ __device__ __forceinline__ bool counts_as_one(float z, float m, float c) {
 
 // The partials of a warp's lanes as one, in every lane.
 __device__ __forceinline__ Partial warp_join(Partial x, float c, bool greedy) {
-  float m = x.m;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  const float m = warp_max(x.m);
   if (greedy) {
     float first = x.m == m ? x.s : kNoPlace;
 #pragma unroll
@@ -168,17 +172,6 @@ __device__ __forceinline__ Partial join_row(const Partial* partials, int parts, 
     x = lane_join(x, {y.x, y.y}, c, greedy);
   }
   return warp_join(x, c, greedy);
-}
-
-// A row's partial over the CTA, from each warp's; in the lanes of one warp (true there).
-__device__ __forceinline__ bool block_join(Partial& x, int j, float c, bool greedy, Partial* s_part) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  Partial* slot = s_part + (j & 1) * kWarps;
-  if (lane == 0) slot[warp] = x;
-  __syncthreads();
-  if (warp != j % kWarps) return false;
-  x = warp_join(lane < kWarps ? slot[lane] : Partial{-INFINITY, greedy ? kNoPlace : 0.f}, c, greedy);
-  return true;
 }
 
 // Notes in words, by entry, what the history and the drafts before row `said` say of the entries
@@ -343,7 +336,7 @@ template <class T, bool kVector, bool kLists, bool kWrite>
 __global__ void __launch_bounds__(kThreads, kBlocks) probs_kernel(const __grid_constant__ ProbsArgs a, int b0, int rows_each,
                                                                   int parts, Lists lists, Partial* partials) {
   __shared__ __align__(16) unsigned char s_gathered[kLists && !kWrite ? sizeof(Gathered) : 16];
-  __shared__ Partial s_part[kWrite ? kRowBlock : 2 * kWarps];
+  __shared__ Partial s_part[kWrite ? kRowBlock : kRowBlock * kWarps];
   extern __shared__ float s_bias[];
   Gathered& g = *reinterpret_cast<Gathered*>(s_gathered);
   const int chunk = blockIdx.x, b = b0 + blockIdx.y, V = a.V, S = a.S;
@@ -440,8 +433,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) probs_kernel(const __grid_c
 #pragma unroll
       for (int i = 0; i < kItems; ++i) x.m = fmaxf(x.m, z[i]);
       // (a warp's maximum, so that its lanes' sums add up without weights)
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) x.m = fmaxf(x.m, __shfl_xor_sync(0xFFFFFFFFu, x.m, o));
+      x.m = warp_max(x.m);
       if (greedy) {
 #pragma unroll
         for (int i = 0; i < kItems; ++i)
@@ -461,7 +453,18 @@ __global__ void __launch_bounds__(kThreads, kBlocks) probs_kernel(const __grid_c
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) x.s += __shfl_xor_sync(0xFFFFFFFFu, x.s, o);
       }
-      if (block_join(x, j, c, greedy, s_part) && lane == 0) partials[row * parts + chunk] = x;
+      // (the CTA's warps meet once for many rows)
+      const int at = (j - j0) % kRowBlock;
+      if (lane == 0) s_part[at * kWarps + warp] = x;
+      if (at + 1 == kRowBlock || j + 1 == j1) {
+        __syncthreads();
+        for (int r = warp; r <= at; r += kWarps) {
+          const Partial y =
+              warp_join(lane < kWarps ? s_part[r * kWarps + lane] : Partial{-INFINITY, greedy ? kNoPlace : 0.f}, c, greedy);
+          if (lane == 0) partials[(row - at + r) * parts + chunk] = y;
+        }
+        if (j + 1 < j1) __syncthreads();
+      }
     } else {
       const Partial x = s_part[(j - j0) % kRowBlock];
       const bool usual = ordinary(x.m, c);
