@@ -187,11 +187,28 @@ __device__ __forceinline__ void note_tokens(const ProbsArgs& a, int b, int v0, i
     if (generated) atomicAdd(&words[v - v0], 1u);
   };
   if (a.history) {
+    const int32_t* list = a.history + (size_t)b * a.history_cap;
+    constexpr int kBatch = 8;
+    int v[kBatch];
+    auto load = [&](int i0) {
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int i = i0 + u * (int)blockDim.x + (int)threadIdx.x;
+        v[u] = i < a.history_cap ? list[i] : -1;
+      }
+    };
+    load(0);  // (whatever the length is: that would come first)
     const int len = a.history_len ? min(a.history_len[b], a.history_cap) : a.history_cap;
     const int prompt = a.prompt_len ? a.prompt_len[b] : 0;
-    const int32_t* list = a.history + (size_t)b * a.history_cap;
-#pragma unroll 8
-    for (int i = threadIdx.x; i < len; i += blockDim.x) note(list[i], i >= prompt, kSeen);
+    for (int i0 = 0; i0 < len;) {
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int i = i0 + u * (int)blockDim.x + (int)threadIdx.x;
+        if (i < len) note(v[u], i >= prompt, kSeen);
+      }
+      i0 += kBatch * (int)blockDim.x;
+      if (i0 < len) load(i0);
+    }
   }
   if (a.draft)
     for (int i = threadIdx.x; i < a.S - 1; i += blockDim.x)
