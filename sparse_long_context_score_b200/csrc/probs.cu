@@ -18,7 +18,7 @@
 // stream by a bit each; a kernel behind it adds their share to the row's sums, and one behind the
 // second pass puts their probabilities over what that wrote there, a thread an entry.
 // 16 x 7 rows of 151552 (68 MB of logits, 68 MB of p), us, without lists / with 4096 tokens of
-// history, 32 biases and a mask: 34 / 64.  Tried: a row held in the registers of a cluster of
+// history, 32 biases and a mask: 34 / 56.  Tried: a row held in the registers of a cluster of
 // eight CTAs, one pass (83 / 133: one such CTA fills an SM, and its loads, lists, exchanges and
 // stores follow one another); lists as a number and a bit for every entry (34 / 82: a warp does
 // the repetition's arithmetic wherever one of its lanes needs it); the listed entries treated by
@@ -262,20 +262,20 @@ __device__ __forceinline__ void gather(const ProbsArgs& a, int b, int v0, int v1
 }
 
 // The listed entries: their partials (kWrite false), or their probabilities, over those that the
-// second pass wrote there.  CTA (256 of a sequence's entries, sequence b0 + blockIdx.y, four rows).
-constexpr int kListedRows = 4;
+// second pass wrote there.  CTA (256 of a sequence's entries, sequence b0 + blockIdx.y, row
+// blockIdx.z).  (A CTA for four rows, which finds an entry's count once: 58.6 us the whole call at
+// 16 x 7 rows against 55.9; for two 56.4.)
 template <class T, bool kWrite>
 __global__ void __launch_bounds__(kThreads) probs_listed_kernel(const __grid_constant__ ProbsArgs a, int b0, int chunks,
                                                                 Lists lists, Partial* partials) {
-  __shared__ Partial s_part[kListedRows][kWarps];
-  const int e = blockIdx.x, parts = chunks + gridDim.x, b = b0 + blockIdx.y, V = a.V;
+  __shared__ Partial s_part[kWarps];
+  const int e = blockIdx.x, parts = chunks + gridDim.x, b = b0 + blockIdx.y, j = blockIdx.z, V = a.V;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int j0 = blockIdx.z * kListedRows, rows = min(a.S - j0, kListedRows);
-  const size_t row0 = (size_t)b * a.S + j0;
+  const size_t row = (size_t)b * a.S + j;
   // The second of these kernels starts when all CTAs of the second pass are past their wait, which
   // the lists and the partials are complete behind: it waits for that pass only before it writes,
   // or ends (what comes behind it in the stream takes the pass for done, too).
-  if (!kWrite) {
+  if constexpr (!kWrite) {
     sm100::grid_dep_wait();
     sm100::grid_dep_launch();
   }
@@ -285,64 +285,43 @@ __global__ void __launch_bounds__(kThreads) probs_listed_kernel(const __grid_con
   const bool there = word != kNobody;
   const int v = there ? (int)(word & kEntry) : 0;
   const RowSettings set = row_settings(a, b);
-  if (__syncthreads_or(there)) {
-    float z[kListedRows];
-    uint32_t bits = 0xFu;  // of the mask, a row each
-#pragma unroll
-    for (int i = 0; i < kListedRows; ++i) {
-      z[i] = there && i < rows ? load_f32(static_cast<const T*>(a.logits) + (row0 + i) * V + v) : -INFINITY;
-      if (a.mask && there && i < rows && !((a.mask[(row0 + i) * ((V + 31) / 32) + (v >> 5)] >> (v & 31)) & 1u)) bits &= ~(1u << i);
-    }
-    uint32_t count = there ? generated : 0u;
-    const float bias = there && (word & kBiased) ? given : 0.f;
-    if (a.draft)
-      for (int k = 0; k < j0; ++k) count += a.draft[(size_t)b * a.S + k] == v;
-#pragma unroll
-    for (int i = 0; i < kListedRows; ++i) {
-      if (a.draft && i > 0 && i < rows) count += a.draft[row0 + i - 1] == v;
-      float x = z[i];
-      if ((word & kSeen) || count) x = x > 0.f ? x / set.rep : x * set.rep;
-      if (count) x = x - set.freq * (float)count - set.pres;
-      x += bias;
-      z[i] = there && ((bits >> i) & 1u) ? fmaxf(x, -INFINITY) : -INFINITY;  // NaN becomes -inf
-    }
-    if constexpr (!kWrite) {
-#pragma unroll
-      for (int i = 0; i < kListedRows; ++i) {
-        const Partial y =
-            warp_join({z[i], set.greedy ? (there ? (float)v : kNoPlace) : z[i] == -INFINITY ? 0.f : 1.f}, set.c, set.greedy);
-        if (lane == 0) s_part[i][warp] = y;
-      }
-    } else {
-      if (warp < rows) {
-        const Partial y = join_row(partials + (row0 + warp) * parts, parts, set.c, set.greedy);
-        if (lane == 0) s_part[warp][0] = y;
-      }
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < kListedRows; ++i) {
-        const Partial y = s_part[i][0];
-        if (i >= rows || y.m == -INFINITY) z[i] = 0.f;
-        else if (set.greedy) z[i] = (float)v == y.s ? 1.f : 0.f;
-        else z[i] = (ordinary(y.m, set.c) ? exp2_approx((z[i] - y.m) * set.c) : counts_as_one(z[i], y.m, set.c) ? 1.f : 0.f) / y.s;
-      }
-      sm100::grid_dep_wait();
-#pragma unroll
-      for (int i = 0; i < kListedRows; ++i)
-        if (there && i < rows) a.p[(row0 + i) * V + v] = z[i];
-    }
-  } else if constexpr (kWrite) {  // nothing but gaps
-    sm100::grid_dep_wait();
-  } else if (threadIdx.x < kListedRows * kWarps) {
-    s_part[threadIdx.x / kWarps][threadIdx.x % kWarps] = Partial{-INFINITY, set.greedy ? kNoPlace : 0.f};
+  const Partial none{-INFINITY, set.greedy ? kNoPlace : 0.f};
+  if (!__syncthreads_or(there)) {  // nothing but gaps
+    if constexpr (kWrite) sm100::grid_dep_wait();
+    else if (threadIdx.x == 0) partials[row * parts + chunks + e] = none;
+    return;
   }
+  float z = there ? load_f32(static_cast<const T*>(a.logits) + row * V + v) : -INFINITY;
+  const bool allowed = there && (!a.mask || (a.mask[row * ((V + 31) / 32) + (v >> 5)] >> (v & 31)) & 1u);
+  uint32_t count = there ? generated : 0u;
+  if (a.draft)
+    for (int k = 0; k < j; ++k) count += a.draft[(size_t)b * a.S + k] == v;
+  if ((word & kSeen) || count) z = z > 0.f ? z / set.rep : z * set.rep;
+  if (count) z = z - set.freq * (float)count - set.pres;
+  if (there && (word & kBiased)) z += given;
+  z = allowed ? fmaxf(z, -INFINITY) : -INFINITY;  // NaN becomes -inf
   if constexpr (!kWrite) {
+    Partial x = warp_join({z, set.greedy ? (there ? (float)v : kNoPlace) : z == -INFINITY ? 0.f : 1.f}, set.c, set.greedy);
+    if (lane == 0) s_part[warp] = x;
     __syncthreads();
-    if (warp < rows) {
-      const Partial y =
-          warp_join(lane < kWarps ? s_part[warp][lane] : Partial{-INFINITY, set.greedy ? kNoPlace : 0.f}, set.c, set.greedy);
-      if (lane == 0) partials[(row0 + warp) * parts + chunks + e] = y;
+    if (warp == 0) {
+      x = warp_join(lane < kWarps ? s_part[lane] : none, set.c, set.greedy);
+      if (lane == 0) partials[row * parts + chunks + e] = x;
     }
+  } else {
+    if (warp == 0) {
+      const Partial x = join_row(partials + row * parts, parts, set.c, set.greedy);
+      if (lane == 0) s_part[0] = x;
+    }
+    __syncthreads();
+    const Partial x = s_part[0];
+    float share = 0.f;
+    if (x.m != -INFINITY) {
+      if (set.greedy) share = (float)v == x.s ? 1.f : 0.f;
+      else share = (ordinary(x.m, set.c) ? exp2_approx((z - x.m) * set.c) : counts_as_one(z, x.m, set.c) ? 1.f : 0.f) / x.s;
+    }
+    sm100::grid_dep_wait();
+    if (there) a.p[row * V + v] = share;
   }
 }
 
@@ -717,7 +696,7 @@ cudaError_t launch_passes(const ProbsArgs& a, unsigned char* ws, cudaStream_t st
     long long rows_each = (long long)l.chunks * n * a.S / ((long long)kBlocks * sms);
     rows_each = rows_each < 1 ? 1 : rows_each > a.S ? a.S : rows_each;
     const dim3 grid(l.chunks, n, (unsigned)((a.S + rows_each - 1) / rows_each));
-    const dim3 entry_grid(entry_parts, n, (a.S + kListedRows - 1) / kListedRows);
+    const dim3 entry_grid(entry_parts, n, a.S);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(kThreads);
