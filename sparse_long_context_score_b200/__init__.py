@@ -11,6 +11,7 @@ Names and argument order follow the C ABI in ``include/dsa.h``.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -122,9 +123,15 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:  # (an import statement looks the module up each time)
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream(stream) -> int:
@@ -466,7 +473,8 @@ def _arg(t, kind, shape, name, dev):
     if t is None:
         return None
     try:
-        if t.dtype in _dtypes[kind] and t.device == dev and (shape is None or t.shape == shape) and t.is_contiguous():
+        if (t.dtype in _dtypes[kind] and t.get_device() == dev.index and (shape is None or t.shape == shape)
+                and t.is_contiguous()):
             return t.data_ptr()
     except AttributeError:
         raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}") from None
@@ -497,7 +505,7 @@ def _call(fn, dev, stream, *args):
         raw = torch._C._cuda_getCurrentRawStream(dev.index)
     else:
         raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if dev.index == torch.cuda.current_device():
+    if dev.index == torch._C._cuda_getDevice():
         rc = fn(*args, raw)
     else:
         with torch.cuda.device(dev):
@@ -603,9 +611,9 @@ def dsa_paged_attn(q, cache, table, cu_q, ctx_len, scale: float, out=None, lse=N
             return dsa_paged_attn(q, cache, table, cu_q, ctx_len, scale, out, lse, ws)
     n, H, _ = q.shape
     if out is None:
-        out = torch.empty((n, H, DV), dtype=torch.bfloat16, device=dev)
+        out = q.new_empty((n, H, DV), dtype=torch.bfloat16)
     if lse is None:
-        lse = torch.empty((n, H), dtype=torch.float32, device=dev)
+        lse = q.new_empty((n, H), dtype=torch.float32)
     ptrs, B, pages = _paged(cache, table, cu_q, ctx_len, dev)
     if ws is None:
         ws = paged_workspace(n, B, H, dev)
@@ -615,6 +623,11 @@ def dsa_paged_attn(q, cache, table, cu_q, ctx_len, scale: float, out=None, lse=N
     if n:
         _call(lib().dsa_paged_attn, dev, stream, *args)
     return out, lse
+
+
+@functools.lru_cache(maxsize=64)
+def _probs_room(*sizes):
+    return lib().dsa_probs_workspace_size(*sizes)
 
 
 def dsa_logits_probs(logits, temperature=None, history=None, history_len=None, prompt_len=None, draft=None,
@@ -633,7 +646,7 @@ def dsa_logits_probs(logits, temperature=None, history=None, history_len=None, p
                                     presence, bias_ids, bias_values, mask, out, ws)
     B, S, V = logits.shape
     if out is None:
-        out = torch.empty((B, S, V), dtype=torch.float32, device=dev)
+        out = logits.new_empty((B, S, V), dtype=torch.float32)
     row = (B,)
     cap = nb = 0
     if history is not None:
@@ -653,6 +666,6 @@ def dsa_logits_probs(logits, temperature=None, history=None, history_len=None, p
             _arg(mask, "i32", (B, S, (V + 31) // 32), "mask", dev), _arg(out, "f32", (B, S, V), "out", dev))
     if B and S:
         if ws is None:
-            ws = torch.empty(lib().dsa_probs_workspace_size(B, S, V, cap, nb), dtype=torch.uint8, device=dev)
+            ws = logits.new_empty(_probs_room(B, S, V, cap, nb), dtype=torch.uint8)
         _call(lib().dsa_logits_probs, dev, stream, *args, _arg(ws, "u8", None, "workspace", dev), ws.numel())
     return out
