@@ -626,8 +626,10 @@ def dsa_paged_attn(q, cache, table, cu_q, ctx_len, scale: float, out=None, lse=N
 
 
 @functools.lru_cache(maxsize=64)
-def _probs_room(*sizes):
-    return lib().dsa_probs_workspace_size(*sizes)
+def _probs_room(dev, *sizes):
+    """Bytes of workspace on a device."""
+    with _torch().cuda.device(dev):
+        return lib().dsa_probs_workspace_size(*sizes)
 
 
 def dsa_logits_probs(logits, temperature=None, history=None, history_len=None, prompt_len=None, draft=None,
@@ -665,7 +667,12 @@ def dsa_logits_probs(logits, temperature=None, history=None, history_len=None, p
             _arg(bias_ids, "i32", (B, nb), "bias_ids", dev), _arg(bias_values, "f32", (B, nb), "bias_values", dev), nb,
             _arg(mask, "i32", (B, S, (V + 31) // 32), "mask", dev), _arg(out, "f32", (B, S, V), "out", dev))
     if B and S:
+        size = 0
         if ws is None:
-            ws = logits.new_empty(_probs_room(B, S, V, cap, nb), dtype=torch.uint8)
-        _call(lib().dsa_logits_probs, dev, stream, *args, _arg(ws, "u8", None, "workspace", dev), ws.numel())
+            size = _probs_room(dev, B, S, V, cap, nb)
+            if size:
+                ws = logits.new_empty(size, dtype=torch.uint8)
+        else:
+            size = ws.numel()
+        _call(lib().dsa_logits_probs, dev, stream, *args, _arg(ws, "u8", None, "workspace", dev), size)
     return out

@@ -662,9 +662,8 @@ dsa_status dsa_logits_probs(const void* logits, int dtype, int B, int S, int V, 
   a.V = V;
   a.history_cap = history_cap;
   a.nbias = nbias;
-  if (!workspace || workspace_bytes < probs_workspace_bytes(B, S, V, history ? history_cap : 0, nbias) ||
-      !aligned(workspace, 256))
-    return DSA_ERR_WORKSPACE;
+  const size_t need = probs_workspace_bytes(B, S, V, history ? history_cap : 0, nbias);
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256))) return DSA_ERR_WORKSPACE;
   const size_t entries = (size_t)B * S * V;
   if (overlap(p, entries * 4, logits, entries * (dtype == DSA_F32 ? 4 : 2))) return DSA_ERR_INVALID_ARG;
   return cuda_status(launch_probs(a, workspace, stream));

@@ -724,16 +724,22 @@ cudaError_t launch_passes(const ProbsArgs& a, unsigned char* ws, cudaStream_t st
   return cudaSuccess;
 }
 
+// CTAs of a cluster for each row, or 0: two passes.  Rows that clusters hold all at once take as
+// many CTAs as keep a thread at eight entries or more.  Two CTAs of up to 24 entries a thread share
+// an SM (32 rows of 50257 take 17 us either way); of 40, one, and clusters leave some SMs out
+// (151552, with 1000 tokens of history: 12 rows 16 us against 21 called one by one and 13.1 against
+// 12.6 replayed, 16 rows 28 against 22).
+int row_cluster(int B, int S, int V, int& held) {
+  const int per_cta = 8 * kRowThreads, sms = device_sm_count();
+  const int C = (V + per_cta - 1) / per_cta < kMaxCluster ? (V + per_cta - 1) / per_cta : kMaxCluster;
+  held = (V + C * kRowThreads - 1) / (C * kRowThreads);
+  return held <= kMaxRowItems && (long long)B * S * C <= (held <= 24 ? 2 * sms : sms * 3 / 4) ? C : 0;
+}
+
 template <class T, bool kVector>
 cudaError_t launch(const ProbsArgs& a, unsigned char* ws, cudaStream_t stream) {
-  // Rows that clusters hold, all at once: as many CTAs a row as keep a thread at eight entries or
-  // more, and the fewest entries a thread that hold it.  Two CTAs of up to 24 entries a thread
-  // share an SM (32 rows of 50257 take 17 us either way); of 40, one, and clusters leave some SMs
-  // out (151552, with 1000 tokens of history: 12 rows 17 us against 22, 16 rows 26 against 23).
-  const int per_cta = 8 * kRowThreads, sms = device_sm_count();
-  const int C = (a.V + per_cta - 1) / per_cta < kMaxCluster ? (a.V + per_cta - 1) / per_cta : kMaxCluster;
-  const int held = (a.V + C * kRowThreads - 1) / (C * kRowThreads);
-  if (held <= kMaxRowItems && (long long)a.B * a.S * C <= (held <= 24 ? 2 * sms : sms * 3 / 4)) {
+  int held;
+  if (const int C = row_cluster(a.B, a.S, a.V, held)) {  // the fewest entries a thread that hold a row
     if (held <= 8) return launch_rows<T, 8, kVector>(a, C, stream);
     if (held <= 16) return launch_rows<T, 16, kVector>(a, C, stream);
     if (held <= 24) return launch_rows<T, 24, kVector>(a, C, stream);
@@ -747,7 +753,8 @@ cudaError_t launch(const ProbsArgs& a, unsigned char* ws, cudaStream_t stream) {
 }  // namespace
 
 size_t probs_workspace_bytes(int B, int S, int V, int history_cap, int nbias) {
-  return probs_layout(B, S, V, history_cap, nbias).total;
+  int held;
+  return row_cluster(B, S, V, held) ? 0 : probs_layout(B, S, V, history_cap, nbias).total;
 }
 
 cudaError_t launch_probs(const ProbsArgs& a, void* workspace, cudaStream_t stream) {
