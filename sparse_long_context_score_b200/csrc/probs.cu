@@ -496,9 +496,11 @@ __global__ void __launch_bounds__(kThreads, kBlocks) probs_kernel(const __grid_c
 
 // ---------------------------------------------------------------- few rows
 // One launch: a cluster of up to eight CTAs per row holds it in registers while its maximum and
-// sum are formed, with two exchanges through distributed shared memory.  Few rows are bound by
-// latency and launches (one row of 50257: 13 us against 16 in two passes, on the host in both; 8
-// rows of 151552 with 1000 tokens of history: 16.5 against 24).
+// sum are formed.  Each warp weighs its entries from its own maximum, and one exchange through
+// distributed shared memory joins the warps' pairs (the maximum first, then the sum: 6.1 us
+// instead of 5.3 for one row of 50257, replayed).  Few rows are bound by latency and, called one by
+// one, by launches: 8 rows of 151552 with 1000 tokens of history take 12.4 us against 21 in two
+// passes, replayed 10.1 against 11.3; one row of 50257 8.9 against 14, replayed 5.3 against 4.4.
 constexpr int kRowThreads = 512, kMaxRowItems = 40, kMaxCluster = 8;
 
 // A CTA holds kHeld x 512 consecutive entries, a thread four at a time.  kVector as above.
@@ -506,7 +508,7 @@ template <class T, int kHeld, bool kVector>
 __global__ void __launch_bounds__(kRowThreads) probs_row_kernel(const __grid_constant__ ProbsArgs a, bool lists) {
   using namespace sm100;
   extern __shared__ __align__(16) uint32_t row_words[];  // by entry, when there are lists; behind them logits
-  __shared__ float s_red[kRowThreads / 32], s_peer[2][kMaxCluster];
+  __shared__ Partial s_part[kRowThreads / 32], s_peer[kMaxCluster];
   constexpr int kSlice = kHeld * kRowThreads;
   const int C = gridDim.x, rank = blockIdx.x, row = blockIdx.y, b = row / a.S, j = row - b * a.S, V = a.V;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -583,65 +585,64 @@ __global__ void __launch_bounds__(kRowThreads) probs_row_kernel(const __grid_con
     }
   }
   const uint32_t* mask = a.mask ? a.mask + (size_t)row * ((V + 31) / 32) : nullptr;
-  float m = -INFINITY;
+  Partial x{-INFINITY, set.greedy ? kNoPlace : 0.f};  // the warp's, then the CTA's, then the row's
 #pragma unroll
   for (int i = 0; i < kHeld; i += 4) {
-    const int at = kRowThreads * i + 4 * tid, v = v0 + at;
+    const int v = v0 + kRowThreads * i + 4 * tid;
     const uint32_t bits = mask && v < v1 ? mask[v >> 5] >> (v & 31) : 0xFu;  // (four in a row lie in one word)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       z[i + e] = (bits >> e) & 1u ? fmaxf(z[i + e], -INFINITY) : -INFINITY;  // NaN becomes -inf
-      m = fmaxf(m, z[i + e]);
+      x.m = fmaxf(x.m, z[i + e]);
     }
   }
-  // all CTAs' values of a quantity, combined
-  bool started = false;
-  auto over_row = [&](float v, int which, auto f) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = f(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-    if (lane == 0) s_red[warp] = v;
-    __syncthreads();
-    if (!started) cluster_wait();
-    started = true;
-    if (warp == 0) {
-      v = s_red[lane & (kRowThreads / 32 - 1)];
-#pragma unroll
-      for (int o = kRowThreads / 64; o > 0; o >>= 1) v = f(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-      if (lane < C) st_cluster_u32(cluster_map(smem_u32(&s_peer[which][rank]), lane), __float_as_uint(v));
-    }
-    cluster_sync();
-    v = s_peer[which][0];
-    for (int i = 1; i < C; ++i) v = f(v, s_peer[which][i]);
-    return v;
-  };
-  m = over_row(m, 0, [](float x, float y) { return fmaxf(x, y); });
-  float* p = a.p + (size_t)row * V;
-  float share = 0.f;
+  x.m = warp_max(x.m);
+  const float own = x.m;
   if (set.greedy) {
-    float first = kNoPlace;
 #pragma unroll
     for (int i = 0; i < kHeld; ++i)
-      if (z[i] == m) first = fminf(first, (float)(v0 + kRowThreads * (i / 4 * 4) + 4 * tid + i % 4));
-    first = over_row(first, 1, [](float x, float y) { return fminf(x, y); });
+      if (z[i] == own) x.s = fminf(x.s, (float)(v0 + kRowThreads * (i / 4 * 4) + 4 * tid + i % 4));
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) z[i] = (float)(v0 + kRowThreads * (i / 4 * 4) + 4 * tid + i % 4) == first ? 1.f : 0.f;
-    share = m == -INFINITY ? 0.f : 1.f;
-  } else {
-    const bool usual = ordinary(m, set.c);
+    for (int o = 16; o > 0; o >>= 1) x.s = fminf(x.s, __shfl_xor_sync(0xFFFFFFFFu, x.s, o));
+  } else {  // weights from the warp's maximum
+    const bool usual = ordinary(own, set.c);
     if (!usual) {
 #pragma unroll
-      for (int i = 0; i < kHeld; ++i) z[i] = m != -INFINITY && counts_as_one(z[i], m, set.c) ? 0.f : -INFINITY;
+      for (int i = 0; i < kHeld; ++i) z[i] = own != -INFINITY && counts_as_one(z[i], own, set.c) ? 0.f : -INFINITY;
     }
-    const float from = usual ? m : 0.f, scale = usual ? set.c : 1.f;
-    float sum = 0.f;
+    const float from = usual ? own : 0.f, scale = usual ? set.c : 1.f;
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) {
       z[i] = exp2_approx((z[i] - from) * scale);
-      sum += z[i];
+      x.s += z[i];
     }
-    sum = over_row(sum, 1, [](float x, float y) { return x + y; });
-    share = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x.s += __shfl_xor_sync(0xFFFFFFFFu, x.s, o);
   }
+  const Partial none{-INFINITY, set.greedy ? kNoPlace : 0.f};
+  if (lane == 0) s_part[warp] = x;
+  __syncthreads();
+  cluster_wait();
+  if (warp == 0) {
+    x = warp_join(lane < kRowThreads / 32 ? s_part[lane] : none, set.c, set.greedy);
+    if (lane < C) {
+      const uint32_t to = cluster_map(smem_u32(&s_peer[rank]), lane);
+      st_cluster_u32(to, __float_as_uint(x.m));
+      st_cluster_u32(to + 4, __float_as_uint(x.s));
+    }
+  }
+  cluster_sync();
+  x = warp_join(lane < C ? s_peer[lane] : none, set.c, set.greedy);
+  // what a weight from the warp's maximum is of the row's sum
+  float share = 0.f;
+  if (set.greedy) {
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) z[i] = (float)(v0 + kRowThreads * (i / 4 * 4) + 4 * tid + i % 4) == x.s ? 1.f : 0.f;
+    share = x.m == -INFINITY ? 0.f : 1.f;
+  } else if (own != -INFINITY) {
+    share = (ordinary(x.m, set.c) ? exp2_approx((own - x.m) * set.c) : counts_as_one(own, x.m, set.c) ? 1.f : 0.f) / x.s;
+  }
+  float* p = a.p + (size_t)row * V;
 #pragma unroll
   for (int i = 0; i < kHeld; i += 4) {
     const int v = v0 + kRowThreads * i + 4 * tid;
@@ -746,8 +747,7 @@ cudaError_t launch_passes(const ProbsArgs& a, unsigned char* ws, cudaStream_t st
 // CTAs of a cluster for each row, or 0: two passes.  Rows that clusters hold all at once take as
 // many CTAs as keep a thread at eight entries or more.  Two CTAs of up to 24 entries a thread share
 // an SM (32 rows of 50257 take 17 us either way); of 40, one, and clusters leave some SMs out
-// (151552, with 1000 tokens of history: 12 rows 16 us against 21 called one by one and 13.1 against
-// 12.6 replayed, 16 rows 28 against 22).
+// (151552, with 1000 tokens of history: 12 rows 12.5 us against 21, 16 rows 28 against 22).
 int row_cluster(int B, int S, int V, int& held) {
   const int per_cta = 8 * kRowThreads, sms = device_sm_count();
   const int C = (V + per_cta - 1) / per_cta < kMaxCluster ? (V + per_cta - 1) / per_cta : kMaxCluster;
