@@ -18,7 +18,7 @@
 // stream by a bit each; a kernel behind it adds their share to the row's sums, and one behind the
 // second pass puts their probabilities over what that wrote there, a thread an entry.
 // 16 x 7 rows of 151552 (68 MB of logits, 68 MB of p), us, without lists / with 4096 tokens of
-// history, 32 biases and a mask: 34 / 56.  Tried: a row held in the registers of a cluster of
+// history, 32 biases and a mask: 34 / 55.  Tried: a row held in the registers of a cluster of
 // eight CTAs, one pass (83 / 133: one such CTA fills an SM, and its loads, lists, exchanges and
 // stores follow one another); lists as a number and a bit for every entry (34 / 82: a warp does
 // the repetition's arithmetic wherever one of its lanes needs it); the listed entries treated by
@@ -747,7 +747,8 @@ cudaError_t launch_passes(const ProbsArgs& a, unsigned char* ws, cudaStream_t st
 // CTAs of a cluster for each row, or 0: two passes.  Rows that clusters hold all at once take as
 // many CTAs as keep a thread at eight entries or more.  Two CTAs of up to 24 entries a thread share
 // an SM (32 rows of 50257 take 17 us either way); of 40, one, and clusters leave some SMs out
-// (151552, with 1000 tokens of history: 12 rows 12.5 us against 21, 16 rows 28 against 22).
+// (151552, with 1000 tokens of history: 12 rows 12.5 us against 21, 16 rows 20.8 either way and
+// 18.6 against 14.3 replayed).
 int row_cluster(int B, int S, int V, int& held) {
   const int per_cta = 8 * kRowThreads, sms = device_sm_count();
   const int C = (V + per_cta - 1) / per_cta < kMaxCluster ? (V + per_cta - 1) / per_cta : kMaxCluster;
