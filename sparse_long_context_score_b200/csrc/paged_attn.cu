@@ -87,9 +87,14 @@ __device__ __forceinline__ int tile_at(const Segment& s, int i) {
   return k < s.k1 ? k : k - (s.k1 - s.k0);
 }
 
+// Query rows of a sequence and the cached rows that they see.
+struct SequenceWork {
+  int tiles, rows, row0, seen0, limit;
+};
 // A CTA's share: it starts `at` into query tile `tile` of sequence b (-1: nowhere).
 struct Share {
   int b, tile, at, length;
+  SequenceWork work;  // of that sequence
 };
 // A query tile that CTA g begins and later CTAs go on with, for the combine.
 struct Join {
@@ -108,13 +113,14 @@ constexpr int kOffVote = kOffM + 64 * 4;             // [2] u32: a half of the r
 constexpr int kOffOver = kOffVote + 16;              // u32: number of the last guessed tile that exceeded the maximum
 constexpr int kOffBad = kOffOver + 16;               // u32: 16-row groups of the tile that are not there
 constexpr int kOffShare = kOffBad + 16;
-constexpr int kOffSum = kOffShare + 16;              // [12] i64: per warp
+constexpr int kOffSum = kOffShare + 48;              // [12] i64: per warp
 constexpr int kOffSeg = kOffSum + kThreadsP / 32 * 8;
 constexpr int kOffBar = kOffSeg + kSegs * (int)sizeof(Segment) + 16;
 constexpr int kNumBars = 10 + 2 * kSegs + 8;
 constexpr int kOffTmem = kOffBar + kNumBars * 8;
 constexpr int kSmemP = kOffTmem + 16 + 1024;         // + alignment slack
 static_assert(kOffBar % 8 == 0, "barrier alignment");
+static_assert(sizeof(Share) <= 48, "a share's place");
 static_assert(kSmemP <= 232448, "shared memory budget");
 
 constexpr int kTmemO = 0;      // O^T: 4 blocks x 64 columns, all 128 lanes
@@ -161,14 +167,11 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-// Query rows of a sequence and the cached rows that they see.
-struct SequenceWork {
-  int tiles, rows, seen0, limit;
-};
 __device__ __forceinline__ SequenceWork sequence_work(const PagedBatch& p, int b, int H) {
   const int q0 = p.cu_q[b], q1 = p.cu_q[b + 1];
   SequenceWork w;
   w.rows = q0 < 0 ? 0 : max(min(q1, p.n) - q0, 0) * H;
+  w.row0 = q0 * H;
   w.tiles = (w.rows + kRows - 1) / kRows;
   // (below 2^31 by two key tiles, so that a tile's end stays an int)
   w.limit = (int)max(0LL, min(min((long long)p.ctx_len[b], 0x7FFFFF00LL), (long long)p.max_pages * p.page_size));
@@ -259,7 +262,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
   {
     long long* s_sum = reinterpret_cast<long long*>(smem + kOffSum);
     long long total = 0, own = 0, before = 0;
-    SequenceWork w{0, 0, 0, 0};
+    SequenceWork w{0, 0, 0, 0, 0};
     auto scan = [&](int b0) {  // work of sequence b0 + threadIdx.x, the sum before it, the sum of all 384
       const int b = b0 + threadIdx.x;
       own = 0;
@@ -287,7 +290,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
     };
     for (int b0 = 0; b0 < p.B; b0 += kThreadsP) total += scan(b0);
     const long long per = max(1LL, (total + gridDim.x - 1) / gridDim.x), start = per * cta;
-    if (threadIdx.x == 0) *s_share = Share{-1, 0, 0, 0};
+    if (threadIdx.x == 0) s_share->b = -1;
     long long base = 0;
     for (int b0 = 0; b0 < p.B; b0 += kThreadsP) {
       long long all = total;
@@ -301,7 +304,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
           if (work_before(w, mid, H) <= at) lo = mid;
           else hi = mid - 1;
         }
-        *s_share = Share{b0 + (int)threadIdx.x, lo, (int)(at - work_before(w, lo, H)), (int)min(per, 0x7FFFFFFFLL)};
+        *s_share = Share{b0 + (int)threadIdx.x, lo, (int)(at - work_before(w, lo, H)), (int)min(per, 0x7FFFFFFFLL), w};
       }
       base += all;
     }
@@ -337,8 +340,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
       int b = first.b, tile = first.tile, k0 = max(0, first.at - kTileCost);
       int left = first.length - max(0, kTileCost - first.at);
       Join join{0, 0, 0, 0};
-      SequenceWork w{0, 0, 0, 0};
-      if (b >= 0) w = sequence_work(p, b, H);
+      SequenceWork w = first.work;
       for (int i = 0;; ++i) {
         const int at = i % kSegs;
         Segment s;
@@ -351,7 +353,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
           const int keys = tile_keys(w, tile, H);
           s.b = b;
           s.tile_row = kRows * tile;
-          s.row0 = p.cu_q[b] * H + s.tile_row;
+          s.row0 = w.row0 + s.tile_row;
           s.nrows = min(kRows, w.rows - s.tile_row);
           s.k0 = k0;
           s.k1 = min(keys, k0 + left);
@@ -401,6 +403,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
       auto page_row = [&](int n) {  // pool row of this lane's box in the n-th key tile, -1 where there is none
         if (lane >= boxes || n >= count) return -1;
         const long long pos = (long long)kKeys * tile_at(s, n) + box * lane;
+        if (pos >= s.limit) return -1;
         const long long i = pos / p.page_size;
         if (i >= p.max_pages) return -1;
         const int page = table[i];
@@ -430,7 +433,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
         const uint32_t there = __ballot_sync(0xFFFFFFFFu, row >= 0);
         uint32_t bad = 0;  // per 16 rows
         for (int i = 0; i < kKeys / 16; ++i) bad |= ((there >> (i * 16 / box)) & 1u ? 0u : 1u) << i;
-        const int y = row >= 0 ? row : 0;
+        const int y = row >= 0 ? row : p.num_pages * p.page_size;  // behind the pool: zeros
 #pragma unroll
         for (int i = 0; i < 5; ++i) {  // blocks 2i, 2i + 1; the rotary block alone
           ok &= mbar_wait(free_bar(i), (it & 1) ^ 1, err, 44);
@@ -678,12 +681,13 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
           // A weight of zero does not silence a value of NaN or infinity.  Rows that no query row
           // of the tile sees may hold anything: as values they are zero.  Of a row that some see,
           // only such entries become zero: S has them, so where the row is seen they count.
-          const int first = bad != 0 ? 0 : max(0, seen_first - kKeys * k);
-          for (int x = 64 * first + st; x < kKeys * 64; x += kSoftmaxThreads) {  // (row, 16-byte chunk of 8 blocks)
-            const int row = x >> 6, blk = (x >> 3) & 7, ch = x & 7;
-            uint4* at = reinterpret_cast<uint4*>(smem + kOffStage + blk * kBlockBytes + row * 128 + ch * 16);
-            if (kKeys * k + row >= seen_last || ((bad >> (row >> 4)) & 1u)) *at = make_uint4(0, 0, 0, 0);
-            else if (kKeys * k + row >= seen_first) *at = finite_bf16(*at);
+          // (Boxes without a page or behind the context were loaded as zeros.)
+          const int past = s.limit - kKeys * k, end = min(kKeys, (past + box - 1) & -box);
+          const int chunk = (st >> 3 & 7) * kBlockBytes + (st & 7) * 16;  // a thread's 16 bytes of a row
+#pragma unroll 4
+          for (int row = max(0, seen_first - kKeys * k) + (st >> 6); row < end; row += kSoftmaxThreads / 64) {
+            uint4* at = reinterpret_cast<uint4*>(smem + kOffStage + chunk + row * 128);
+            *at = kKeys * k + row >= seen_last ? make_uint4(0, 0, 0, 0) : finite_bf16(*at);
           }
         }
         fence_proxy_async();  // P (and the zeros) are visible to the tensor core
