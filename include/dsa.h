@@ -479,7 +479,8 @@ dsa_status dsa_paged_attn(const uint16_t *q, const uint16_t *cache, const int32_
  * Ids outside [0, V) are skipped (padding).  p must not overlap an input.
  * workspace: dsa_probs_workspace_size bytes (history_cap 0 without a history), 256-byte aligned,
  * written by every call (calls that overlap on the GPU need one each); the size depends on the
- * current device.  Few rows need none: the size is 0, and workspace may be NULL.  S <= 65535,
+ * current device.  Few rows need none: the size is 0 (as it is for sizes out of range), and
+ * workspace may be NULL.  S <= 65535,
  * nbias <= 4096 (biases are few: one on much of the vocabulary belongs in the logits).
  */
 size_t dsa_probs_workspace_size(int B, int S, int V, int history_cap, int nbias);

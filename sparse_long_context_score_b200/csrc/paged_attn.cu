@@ -634,7 +634,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
 #pragma unroll
           for (int r = 0; r < 32; ++r) {
             m[r] = fmaxf(__shfl_sync(0xFFFFFFFFu, mrow, r), kNoMax);
-            l[r] *= __shfl_sync(0xFFFFFFFFu, alpha, r);
+          }
+          if (scaled) {
+#pragma unroll
+            for (int r = 0; r < 32; ++r) l[r] *= __shfl_sync(0xFFFFFFFFu, alpha, r);
           }
           if (n > 0) {
             if (quarter == 0) {
