@@ -612,13 +612,18 @@ def dsa_paged_attn(q, cache, table, cu_q, ctx_len, scale: float, out=None, lse=N
     n, H, _ = q.shape
     if out is None:
         out = q.new_empty((n, H, DV), dtype=torch.bfloat16)
+        out_ptr = out.data_ptr()
+    else:
+        out_ptr = _arg(out, "bf16", (n, H, DV), "out", dev)
     if lse is None:
         lse = q.new_empty((n, H), dtype=torch.float32)
+        lse_ptr = lse.data_ptr()
+    else:
+        lse_ptr = _arg(lse, "f32", (n, H), "lse", dev)
     ptrs, B, pages = _paged(cache, table, cu_q, ctx_len, dev)
     if ws is None:
         ws = paged_workspace(n, B, H, dev)
-    args = (_arg(q, "bf16", (n, H, DQK), "q", dev), *ptrs, n, B, H, *pages, float(scale),
-            _arg(out, "bf16", (n, H, DV), "out", dev), _arg(lse, "f32", (n, H), "lse", dev),
+    args = (_arg(q, "bf16", (n, H, DQK), "q", dev), *ptrs, n, B, H, *pages, float(scale), out_ptr, lse_ptr,
             _arg(ws, "u8", None, "workspace", dev), ws.numel())
     if n:
         _call(lib().dsa_paged_attn, dev, stream, *args)
