@@ -17,7 +17,9 @@
 // about the same time, and the shares' borders shift from tile to tile.  So every CTA starts where
 // its key tile's number is a multiple of the share's length, and takes the ones before that
 // last: at any time the CTAs of a sequence are at the same few places (16 sequences of 2 to 8 new
-// tokens x 64 heads over 4K to 32K: 1.29 -> 0.73 GB from HBM, 371 -> 351 us).
+// tokens x 64 heads over 4K to 32K: 1.29 -> 0.73 GB from HBM, 371 -> 351 us).  (Prefetching two
+// key tiles ahead into L2 on top of that gained 3 to 6% in short bursts of such calls, and lost 2 to
+// 4% of decode and of many sequences once the power limit is met.)
 //
 // One key tile of a CTA, everything in shared memory beside the 64 query rows (73.7 KB):
 //   S^T = K Q^T     M = 128 keys, N = 64 rows, K = 576        (36 MMAs; TMEM lane = key)
@@ -60,7 +62,6 @@ constexpr int kLoadWarp = 0, kMmaWarp = 1, kQueryWarp = 2, kWalkWarp = 3, kSoftm
 constexpr int kSoftmaxThreads = 256;             // eight warps: two per TMEM lane quarter
 constexpr int kThreadsP = kSoftmaxWarp0 * 32 + kSoftmaxThreads;  // 384
 constexpr float kRescaleLog2 = 8.f;
-constexpr int kPrefetchTiles = 64;
 // Beginning a query tile costs a CTA as much as so many key tiles: the end of the one before
 // (maxima, sums, 131 KB of values) and a first key tile that nothing runs ahead of take 10K cycles
 // more than the 5.4K of a key tile.  Shares of equal key tiles: 16 verify chunks 340 us instead of
@@ -77,7 +78,6 @@ struct Segment {
   int turn;
   int seen0;     // cached rows that the sequence's first new token sees
   int limit;     // cached rows of the sequence
-  int tiles;     // query tiles of the sequence
   int part;      // workspace slot of this part of the tile; -1: the tile is whole
 };
 
@@ -206,7 +206,7 @@ __device__ __forceinline__ long long work_before(const SequenceWork& w, int tile
 
 __global__ void __launch_bounds__(kThreadsP, 1)
 paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap cmap,
-                  const __grid_constant__ CUtensorMap rmap, PagedBatch p, int H, int box, float scale_log2, uint32_t negate, const uint16_t* cache, uint16_t* out, float* lse, Join* joins, float* parts, float2* part_ml, int* err) {
+                  const __grid_constant__ CUtensorMap rmap, PagedBatch p, int H, int box, float scale_log2, uint32_t negate, uint16_t* out, float* lse, Join* joins, float* parts, float2* part_ml, int* err) {
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   const uint32_t sbase = smem_u32(smem);
@@ -359,7 +359,6 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
           s.k1 = min(keys, k0 + left);
           s.seen0 = w.seen0;
           s.limit = w.limit;
-          s.tiles = w.tiles;
           s.part = k0 > 0 ? 2 * cta : s.k1 < keys ? 2 * cta + 1 : -1;
           if (k0 == 0 && s.k1 < keys) join = Join{s.row0, s.nrows, 1 + (keys - s.k1 + first.length - 1) / first.length, 0};
           const int next_phase = (k0 + first.length - 1) / first.length * first.length;  // a multiple of the share
@@ -410,24 +409,6 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
         return page >= 0 && page < p.num_pages ? page * p.page_size + (int)(pos - i * p.page_size) : -1;
       };
       int row = page_row(0), next = page_row(1);
-      // A context that few query tiles read comes mostly from HBM: its tiles are brought into L2
-      // two ahead, so that the stream goes on while the blocks of shared memory are in use (2 to 8
-      // tokens x 64 heads: 354 -> 338 us; one token: HBM is busy either way; a prefill chunk's 512
-      // tiles: 1% slower).  By plain prefetches: the copy engine takes as long for a prefetched
-      // tile as for a loaded one.
-      const bool from_hbm = s.tiles <= kPrefetchTiles;
-      auto prefetch = [&](int r) {
-        if (!from_hbm) return;
-#pragma unroll
-        for (int i = 0; i < kKeys / 32; ++i) {
-          const int y = 32 * i + lane, base = __shfl_sync(0xFFFFFFFFu, r, y / box);
-          if (base < 0) continue;
-          const char* line = reinterpret_cast<const char*>(cache) + ((size_t)base + y % box) * (kDqk * 2);
-#pragma unroll
-          for (int j = 0; j < kBlocks; ++j) asm volatile("prefetch.global.L2 [%0];" ::"l"(line + 128 * j));
-        }
-      };
-      prefetch(next);
       for (int n = 0; n < count; ++n, ++it) {
         const int ahead = page_row(n + 2);
         const uint32_t there = __ballot_sync(0xFFFFFFFFu, row >= 0);
@@ -455,7 +436,6 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
         }
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
-        prefetch(ahead);
         row = next;
         next = ahead;
       }
@@ -911,7 +891,7 @@ cudaError_t launch_paged_attn(const uint16_t* q, const uint16_t* cache, const Pa
   float2* part_ml = reinterpret_cast<float2*>(ws + l.part_ml);
   float* parts = reinterpret_cast<float*>(ws + l.parts);
   paged_attn_kernel<<<ctas, kThreadsP, kSmemP, stream>>>(qmap, cmap, rmap, p, H, box, fabsf(scale) * 1.4426950408889634f,
-                                                         scale < 0.f ? 1u << 13 : 0u, cache, out, lse, joins, parts, part_ml, err);
+                                                         scale < 0.f ? 1u << 13 : 0u, out, lse, joins, parts, part_ml, err);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // waits in-kernel
