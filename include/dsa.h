@@ -436,7 +436,7 @@ dsa_status dsa_cache_append(const uint16_t *x, long long x_stride, const uint16_
 
 /*
  * Attention of the new tokens over their sequences' cached rows (the new ones among them):
- *   q    [n, H, 576] bf16        1 <= H <= 128
+ *   q    [n, H, 576] bf16        1 <= H <= 128, n H <= 2^31 - 256
  *   out  [n, H, 512] bf16  out:  softmax_s(scale * q . c[s]) weighted sum of c[s][0:512] over
  *                                the positions s <= the token's own; zero when it sees none
  *   lse  [n, H] f32 out:         ln sum_s exp(scale * q . c[s]) (-inf when none); may be NULL
@@ -480,7 +480,7 @@ dsa_status dsa_paged_attn(const uint16_t *q, const uint16_t *cache, const int32_
  * workspace: dsa_probs_workspace_size bytes (history_cap 0 without a history), 256-byte aligned,
  * written by every call (calls that overlap on the GPU need one each); the size depends on the
  * current device.  Few rows need none: the size is 0 (as it is for sizes out of range), and
- * workspace may be NULL.  S <= 65535,
+ * workspace may be NULL.  S <= 4096,
  * nbias <= 4096 (biases are few: one on much of the vocabulary belongs in the logits).
  */
 size_t dsa_probs_workspace_size(int B, int S, int V, int history_cap, int nbias);

@@ -592,7 +592,7 @@ dsa_status dsa_cache_append(const uint16_t* x, long long x_stride, const uint16_
 }
 
 size_t dsa_paged_workspace_size(int n, int B, int H) {
-  if (n < 0 || B <= 0 || H <= 0 || H > 128 || (long long)n * H > 0x7FFFFFFFLL) return 0;
+  if (n < 0 || B <= 0 || H <= 0 || H > 128 || (long long)n * H > 0x7FFFFF00LL) return 0;
   return paged_attn_workspace_bytes();
 }
 
@@ -604,7 +604,7 @@ dsa_status dsa_paged_attn(const uint16_t* q, const uint16_t* cache, const int32_
   const dsa_status st = check_paged(cache, table, cu_q, ctx_len, n, B, num_pages, page_size, max_pages);
   if (st != DSA_OK) return st;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4)) return DSA_ERR_INVALID_ARG;
-  if (H > 128 || (long long)n * H > 0x7FFFFFFFLL) return DSA_ERR_UNSUPPORTED;
+  if (H > 128 || (long long)n * H > 0x7FFFFF00LL) return DSA_ERR_UNSUPPORTED;
   if (n == 0) return DSA_OK;
   const size_t rows = (size_t)n * H, pool = (size_t)num_pages * page_size * kDqk * 2;
   if (overlap(out, rows * kDv * 2, q, rows * kDqk * 2) || overlap(out, rows * kDv * 2, cache, pool) ||
@@ -619,7 +619,7 @@ dsa_status dsa_paged_attn(const uint16_t* q, const uint16_t* cache, const int32_
 }
 
 size_t dsa_probs_workspace_size(int B, int S, int V, int history_cap, int nbias) {
-  if (B <= 0 || S <= 0 || S > 65535 || V <= 0 || V >= (1 << 24) || (long long)B * S > 0x7FFFFFFFLL || history_cap < 0 ||
+  if (B <= 0 || S <= 0 || S > 4096 || V <= 0 || V >= (1 << 24) || (long long)B * S > 0x7FFFFFFFLL || history_cap < 0 ||
       history_cap >= (1 << 28) || nbias < 0 || nbias > 4096)
     return 0;
   return probs_workspace_bytes(B, S, V, history_cap, nbias);
@@ -635,7 +635,7 @@ dsa_status dsa_logits_probs(const void* logits, int dtype, int B, int S, int V, 
       (long long)B * S > 0x7FFFFFFFLL || (nbias > 0 && (!bias_ids || !bias_values)))
     return DSA_ERR_INVALID_ARG;
   if (dtype != DSA_BF16 && dtype != DSA_F32) return DSA_ERR_UNSUPPORTED;
-  if (history_cap >= (1 << 28) || nbias > 4096 || S > 65535) return DSA_ERR_UNSUPPORTED;
+  if (history_cap >= (1 << 28) || nbias > 4096 || S > 4096) return DSA_ERR_UNSUPPORTED;
   if (!aligned(logits, dtype == DSA_F32 ? 4 : 2)) return DSA_ERR_INVALID_ARG;
   const void* words[] = {p,       temperature, repetition, frequency, presence,    history,
                          history_len, prompt_len,  draft,      bias_ids,  bias_values, mask};

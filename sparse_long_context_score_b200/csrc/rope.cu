@@ -211,8 +211,9 @@ __global__ void __launch_bounds__(32 * kAppendWarps) append_kernel(const uint16_
                                                                    const __grid_constant__ dsa_rope_plan plan,
                                                                    PagedBatch pb, uint16_t* __restrict__ cache) {
   using B16 = Chunk<__nv_bfloat16>;
-  const int token = blockIdx.x * kAppendWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (token >= pb.n) return;
+  const long long at = (long long)blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
+  if (at >= pb.n) return;
+  const int token = (int)at, lane = threadIdx.x & 31;
   const uint4* src = reinterpret_cast<const uint4*>(x + token * x_stride);
   const uint4* gm = reinterpret_cast<const uint4*>(gamma);
   const uint4 c0 = src[lane], c1 = src[32 + lane], g0 = gm[lane], g1 = gm[32 + lane];
@@ -322,7 +323,7 @@ cudaError_t launch_rope(const void* x, const long long* positions, long long n, 
 
 cudaError_t launch_cache_append(const uint16_t* x, long long x_stride, const uint16_t* gamma, float eps,
                                 const dsa_rope_plan& plan, const PagedBatch& pb, uint16_t* cache, cudaStream_t stream) {
-  append_kernel<<<(unsigned)((pb.n + kAppendWarps - 1) / kAppendWarps), 32 * kAppendWarps, 0, stream>>>(x, x_stride, gamma,
+  append_kernel<<<(unsigned)((pb.n + kAppendWarps - 1LL) / kAppendWarps), 32 * kAppendWarps, 0, stream>>>(x, x_stride, gamma,
                                                                                                        eps, plan, pb, cache);
   return cudaGetLastError();
 }

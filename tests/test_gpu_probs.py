@@ -95,6 +95,14 @@ def test_vocabularies_beyond_the_second_level_cache(dsa):
     _check(dsa, _inputs(37, 3, 325001, seed=3, hist=100, bias=3, spread=True, greedy=(36,)))
 
 
+def test_the_most_positions(dsa):
+    """4096 positions, each with the drafts before it."""
+    a = _inputs(1, 4096, 130, seed=12, hist=5)
+    a["draft"] = torch.randint(0, 130, (1, 4096), generator=_gen(13), device="cuda", dtype=torch.int32)
+    a["frequency"], a["presence"] = torch.full((1,), 0.01, device="cuda"), torch.full((1,), 0.5, device="cuda")
+    _check(dsa, a)
+
+
 def test_very_many_short_rows(dsa):
     """A CTA takes all 80 rows of a sequence."""
     z = torch.randn((600, 80, 64), generator=_gen(6), device="cuda") * 4

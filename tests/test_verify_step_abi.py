@@ -147,9 +147,9 @@ def test_logits_probs_refusals(L):
     assert more > need
     assert call(cap=5000, history=FAKE, nbias=4, bias_ids=FAKE, bias_values=FAKE, size=more - 1) == -3
     assert call() == -1 and call(p=AT + 600 * 4 - 4) == -1 and call(p=AT + 600 * 2 - 4, dtype=0) == -1  # p over the logits
-    assert call(S=65536) == -2 and call(nbias=4097, bias_ids=FAKE, bias_values=FAKE) == -2
+    assert call(S=4097) == -2 and call(nbias=4097, bias_ids=FAKE, bias_values=FAKE) == -2
     for sizes in [(0, 1, 10, 0, 0), (1, 0, 10, 0, 0), (1, 1, 0, 0, 0), (1, 1, 1 << 24, 0, 0), (1 << 20, 1 << 20, 10, 0, 0),
-                  (1, 1, 10, -1, 0), (1, 1, 10, 0, -1), (1, 65536, 10, 0, 0), (1, 1, 10, 1 << 28, 0), (1, 1, 10, 0, 4097)]:
+                  (1, 1, 10, -1, 0), (1, 1, 10, 0, -1), (1, 4097, 10, 0, 0), (1, 1, 10, 1 << 28, 0), (1, 1, 10, 0, 4097)]:
         assert L.dsa_probs_workspace_size(*sizes) == 0
 
 
