@@ -332,3 +332,64 @@ def test_a_verify_step_over_a_paged_cache(dsa):
         flags = accept[b].tolist() + [0]
         assert int(length[b]) == flags.index(0)
     assert dsa.dsa_check_device_status() == 0
+
+
+def test_a_captured_verify_step_equals_the_calls_one_by_one(dsa):
+    """The five calls in one graph, replayed while lengths, pages, drafts and histories change; the
+    batch is padded."""
+    H, page, V, S, pool = 16, 64, 60001, 3, 40
+    plan = dsa.dsa_rope_init(64, "half", 1e4, 4.0, 4096)
+    gamma = torch.ones(DV, device="cuda", dtype=torch.bfloat16)
+    n = 2 * (S + 1) + 3
+    bf = lambda *s: torch.zeros(s, device="cuda", dtype=torch.bfloat16)  # noqa: E731
+    ints = lambda *s: torch.zeros(s, device="cuda", dtype=torch.int32)  # noqa: E731
+    a = dict(q=bf(n, H, DQK), x=bf(n, DQK), positions=torch.zeros(n, dtype=torch.int64, device="cuda"),
+             cache=bf(pool, page, DQK), table=ints(2, 16), cu_q=ints(3), ctx=ints(2), logits=torch.zeros((2, S, V), device="cuda"),
+             drafter=torch.zeros((2, S, V), device="cuda"), history=ints(2, 600), length=ints(2), draft=ints(2, S),
+             u=torch.zeros((2, S), device="cuda"), u2=torch.zeros((2, S), device="cuda"),
+             r=torch.full((2,), 1.2, device="cuda"))
+
+    def step(a):
+        dsa.dsa_rope(a["q"][..., DV:], a["positions"], plan, out=a["q"][..., DV:])
+        dsa.dsa_cache_append(a["x"], gamma, 1e-6, plan, a["cache"], a["table"], a["cu_q"], a["ctx"])
+        out, lse = dsa.dsa_paged_attn(a["q"], a["cache"], a["table"], a["cu_q"], a["ctx"], 1 / 24)
+        kw = dict(history=a["history"], history_len=a["length"], draft=a["draft"], repetition=a["r"])
+        p, qp = dsa.dsa_logits_probs(a["logits"], **kw), dsa.dsa_logits_probs(a["drafter"], **kw)
+        return out, lse, p, qp, *dsa.dsa_verify(p, qp, a["draft"], a["u"], a["u2"])
+
+    def fill(seed, new, ctx):
+        g = _gen(seed)
+        batch = Batch(new, ctx, page, seed=seed)
+        for name in ("q", "x", "logits", "drafter", "cache"):
+            a[name].normal_(generator=g)
+        for name in ("u", "u2"):
+            a[name].uniform_(generator=g)
+        a["history"].random_(0, V, generator=g)
+        a["draft"].random_(0, V, generator=g)
+        a["length"].copy_(torch.tensor([17 * seed, 600 - seed]))
+        a["table"].fill_(-1)
+        a["table"][:, :batch.table.shape[1]] = batch.table
+        a["cu_q"].copy_(batch.cu_q)
+        a["ctx"].copy_(batch.ctx_len)
+        a["positions"].fill_(0)
+        a["positions"][:batch.n] = torch.cat([torch.arange(c - k, c) for k, c in zip(new, ctx)]).cuda()
+        return batch.n
+
+    fill(1, [4, 4], [700, 100])
+    step(a)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(a)
+    for seed, new, ctx in [(2, [4, 4], [704, 104]), (3, [1, 4], [900, 4]), (4, [4, 0], [63, 0])]:
+        m = fill(seed, new, ctx)
+        same = {k: v.clone() for k, v in a.items()}
+        graph.replay()
+        torch.cuda.synchronize()
+        want = step(same)
+        torch.cuda.synchronize()
+        assert torch.equal(a["cache"], same["cache"]) and torch.equal(a["q"], same["q"])
+        assert torch.equal(got[0][:m], want[0][:m]) and torch.equal(got[1][:m], want[1][:m])
+        for x, y in zip(got[2:], want[2:]):
+            assert torch.equal(x, y)
+    assert dsa.dsa_check_device_status() == 0
