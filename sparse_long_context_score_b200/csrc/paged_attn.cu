@@ -659,12 +659,26 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
           st_shared_v4(prow + (((4 * half + r0 / 8) ^ (lane & 7)) << 4), pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3]),
                        pack_bf16x2(p[4], p[5]), pack_bf16x2(p[6], p[7]));
         }
-        if (!exchange && __any_sync(0xFFFFFFFFu, most > kRescaleFactor) && lane == 0) *s_over = tiles;
+        // One vote for what is rare: a weight above the cap, and a key whose values may be NaN or
+        // infinite (no product with such a value is finite, so that any one row's logit tells).
+        const bool odd = !(fabsf(__uint_as_float(z[0])) < INFINITY);
+        if (__any_sync(0xFFFFFFFFu, most > kRescaleFactor || odd)) {
+          if (!exchange && __any_sync(0xFFFFFFFFu, most > kRescaleFactor) && lane == 0) *s_over = tiles;
+          // A weight of zero does not silence such a value.  A row that all query rows of the tile see
+          // has a weight of zero where its logit is -inf (NaN and +inf make the weight NaN, which stays
+          // so whatever the values are): its values that are not finite become zero.
+          for (uint32_t todo = __ballot_sync(0xFFFFFFFFu, odd && key < seen_first && half == 0); todo; todo &= todo - 1) {
+            const int row = 32 * quarter + __ffs(todo) - 1;
+            for (int c = lane; c < kDv / 8; c += 32) {
+              uint4* at = reinterpret_cast<uint4*>(smem + kOffStage + (c >> 3) * kBlockBytes + (c & 7) * 16 + row * 128);
+              *at = finite_bf16(*at);
+            }
+          }
+        }
         if (!whole) {
-          // A weight of zero does not silence a value of NaN or infinity.  Rows that no query row
-          // of the tile sees may hold anything: as values they are zero.  Of a row that some see,
-          // only such entries become zero: S has them, so where the row is seen they count.
-          // (Boxes without a page or behind the context were loaded as zeros.)
+          // Rows that no query row of the tile sees may hold anything: as values they are zero.  Of a
+          // row that some see, only such entries become zero: S has them, so where the row is seen
+          // they count.  (Boxes without a page or behind the context were loaded as zeros.)
           const int past = s.limit - kKeys * k, end = min(kKeys, (past + box - 1) & -box);
           const int chunk = (st >> 3 & 7) * kBlockBytes + (st & 7) * 16;  // a thread's 16 bytes of a row
 #pragma unroll 4

@@ -357,3 +357,78 @@ def test_binding_refusals(dsa):
     assert err.value.status == -2
     none = dsa.dsa_paged_attn(q[:0], *args)
     assert none[0].shape == (0, 16, DV)
+
+
+class _Without:
+    """A batch as `attention` takes it, some of its cached positions left out: {sequence: positions}."""
+
+    def __init__(self, batch, gone):
+        self.batch, self.gone = batch, gone
+
+    def __getattr__(self, name):
+        return getattr(self.batch, name)
+
+    def rows(self, b, table=None):
+        r = self.batch.rows(b, table)
+        r[self.gone[b]] = -1
+        return r
+
+
+@pytest.mark.parametrize("what", [math.inf, -math.inf])
+@pytest.mark.parametrize("std", [1.0, 8.0])
+@pytest.mark.parametrize("shape", ["chunks", "one long", "short"])
+def test_infinite_latents_under_a_logit_of_minus_infinity(dsa, shape, std, what):
+    """Rows with an infinite latent entry, which is a value too: where a query's sign makes the
+    logit -inf the row weighs nothing, wherever it lies in its key tile, its context or a CTA's share;
+    where it makes it +inf the result is NaN."""
+    H = 64
+    if shape == "chunks":
+        batch = _long_batch(False, 21)
+    elif shape == "one long":
+        batch = Batch([1], [50000], 128, seed=21).fill(seed=21)
+    else:
+        batch = Batch([3, 1, 2], [40, 128, 300], 16, seed=21).fill(seed=21)
+    q = _queries(batch.n, H, std=std)
+    up = (torch.arange(H, device="cuda") * 5 % 7 < 3)
+    columns = (7, 200, 511)
+    for d in columns:
+        q[:, :, d] = torch.where(up, 1.0, -1.0).to(torch.bfloat16)
+    flat, gone = batch.cache.view(-1, DQK), {}
+    for b, (new, ctx) in enumerate(zip(batch.new, batch.ctx)):
+        r = batch.rows(b)
+        at = {0, 1, 63, 127, 128, 700 + 3 * b, 1300, 1301, ctx // 2, ctx - new - 1, ctx - new, ctx - 1} | set(range(900, ctx, 4097))
+        gone[b] = torch.tensor(sorted(s for s in at if 0 <= s < ctx))
+        for i, s in enumerate(gone[b].tolist()):
+            flat[r[s], columns[(i + b) % 3]] = what
+    out, lse = dsa.dsa_paged_attn(q, batch.cache, batch.table, batch.cu_q, batch.ctx_len, SCALE)
+    assert dsa.dsa_check_device_status() == 0
+    nan = up if what > 0 else ~up
+    for b, (new, ctx) in enumerate(zip(batch.new, batch.ctx)):
+        if int(gone[b][0]) <= ctx - new:  # (every token sees one)
+            o, l = out[batch.ends[b]:batch.ends[b + 1], nan], lse[batch.ends[b]:batch.ends[b + 1], nan]
+            assert bool(l.isnan().all()) and bool(o.isnan().all())
+    keep = ~nan
+    want = attention(_Without(batch, gone), q[:, keep].contiguous(), SCALE)
+    b_out, b_lse = attention_bounds(*want, max(batch.ctx))
+    o, l, none = out[:, keep].double(), lse[:, keep].double(), want[1] == -math.inf
+    assert bool(o.isfinite().all())
+    assert bool((l[none] == -math.inf).all()) and bool((o[none] == 0).all())
+    assert bool(((o - want[0]).abs() <= b_out).all())
+    assert bool(((l - want[1]).abs() <= b_lse)[~none].all())
+
+
+@pytest.mark.parametrize("ctx", [100, 30000])
+def test_infinite_latents_that_some_queries_multiply_by_zero(dsa, ctx):
+    """0 x infinity makes those heads' logits NaN; the heads whose logit is -inf do without the row."""
+    batch = Batch([2], [ctx], 64, seed=5).fill(seed=5)
+    q = _queries(2, 64)
+    kind = torch.arange(64, device="cuda") % 3  # 0: NaN, 1: -inf, 2: +inf
+    q[:, :, 40] = torch.where(kind == 0, 0.0, torch.where(kind == 1, -1.0, 1.0)).to(torch.bfloat16)
+    at = torch.tensor([0, 64, ctx // 2, ctx - 3])
+    batch.cache.view(-1, DQK)[batch.rows(0)[at], 40] = math.inf
+    out, lse = dsa.dsa_paged_attn(q, batch.cache, batch.table, batch.cu_q, batch.ctx_len, SCALE)
+    assert bool(out[:, kind != 1].isnan().all()) and bool(lse[:, kind != 1].isnan().all())
+    want = attention(_Without(batch, {0: at}), q[:, kind == 1].contiguous(), SCALE)
+    b_out, b_lse = attention_bounds(*want, ctx)
+    assert bool(((out[:, kind == 1].double() - want[0]).abs() <= b_out).all())
+    assert bool(((lse[:, kind == 1].double() - want[1]).abs() <= b_lse).all())
