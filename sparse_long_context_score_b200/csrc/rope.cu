@@ -178,11 +178,11 @@ __global__ void __launch_bounds__(256) rope_kernel(RopeArgs a, const __grid_cons
 }
 
 // The scale that sums of squares outside [2^-100, 2^120] are taken again under, so that rows
-// of any bf16 magnitude keep their norm (1 otherwise).  Small sums matter only beside a
-// smaller eps.
+// of any bf16 magnitude keep their norm (1 otherwise): entries up to 2^-50 times 2^90 have squares
+// between 2^-86 and 2^80.  Small sums matter only beside a smaller eps.
 __device__ __forceinline__ float norm_rescale(float sum, float eps) {
   if (sum > 0x1p120f) return 0x1p-70f;
-  return sum < 0x1p-100f && eps < 0x1p-90f ? 0x1p70f : 1.f;
+  return sum < 0x1p-100f && eps < 0x1p-90f ? 0x1p90f : 1.f;
 }
 
 // The sequence b with cu_q[b] <= token < cu_q[b + 1], for the lanes of a warp alike; -1 if
@@ -237,15 +237,17 @@ __global__ void __launch_bounds__(32 * kAppendWarps) append_kernel(const uint16_
   float sum = squares(1.f);
   const float s = norm_rescale(sum, eps);
   if (s != 1.f) sum = squares(s);
-  const float inv = rsqrtf(sum / kDv + eps * s * s) * s;
+  // y = x s rsqrt(mean (x s)^2 + eps s^2).  A large s stays with x: times the root, some 2^133 for
+  // entries of 2^-133, it would pass 32 bits.  A small one stays with the root: x s would lose bits.
+  const float up = fmaxf(s, 1.f), inv = rsqrtf(sum / kDv + eps * s * s) * fminf(s, 1.f);
   uint4* dst = reinterpret_cast<uint4*>(cache + row * kDqk);
   B16::unpack(g0, w);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v0[i] = v0[i] * inv * w[i];
+  for (int i = 0; i < 8; ++i) v0[i] = v0[i] * up * inv * w[i];
   dst[lane] = B16::pack(v0);
   B16::unpack(g1, w);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v1[i] = v1[i] * inv * w[i];
+  for (int i = 0; i < 8; ++i) v1[i] = v1[i] * up * inv * w[i];
   dst[32 + lane] = B16::pack(v1);
   const float2 r = rope_angle(position, plan.turns[lane], plan.mscale);
   B16::unpack(cr, v0);

@@ -265,3 +265,35 @@ def test_a_rotation_on_another_stream_keeps_its_result(dsa):
     got = dsa.dsa_rope(x, positions, plan, stream=side)
     torch.cuda.synchronize()
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-45, 1e-38, 1e-30, 1e-12])
+def test_append_rows_of_any_magnitude(dsa, eps):
+    """From the smallest subnormal entries to the largest ones, alone in their row, all alike or of
+    many sizes; without an eps that would hide them."""
+    g, rows = _gen(8), []
+    for size in (2.0 ** -133, 2.0 ** -130, 2.0 ** -128, 2.0 ** -126, 1e-30, 1e-20, 2.0 ** -50, 1.0, 1e18, 1e30, 3.38e38):
+        rows.append(torch.full((DV,), size, device="cuda"))
+        one = torch.zeros(DV, device="cuda")
+        one[17], one[400] = size, -size / 2
+        rows.append(one)
+        rows.append((torch.rand(DV, generator=g, device="cuda") - 0.5) * size)
+        spread = torch.full((DV,), size, device="cuda") * 2.0 ** -torch.arange(DV, device="cuda").remainder(40)
+        rows.append(spread)
+    n = len(rows)
+    x = torch.zeros((n, DQK), device="cuda", dtype=torch.bfloat16)
+    x[:, :DV] = torch.stack(rows).to(torch.bfloat16)
+    batch = Batch([n], [n], 16)
+    gamma = (torch.rand(DV, generator=g, device="cuda") + 0.5).to(torch.bfloat16)
+    flat = dsa.dsa_cache_append(x, gamma, eps, dsa.dsa_rope_init(64), batch.cache, batch.table, batch.cu_q,
+                                batch.ctx_len).view(-1, DQK)
+    y = x[:, :DV].double()
+    # (eps as the 32-bit number that the call takes)
+    want = y / (y.pow(2).mean(-1, keepdim=True) + torch.tensor(eps, dtype=torch.float32).double().item()).sqrt() * gamma.double()
+    got = flat[batch.rows(0).cuda(), :DV].double()
+    # a value below bf16's normal range is off by half of its smallest subnormal, 2^-134, and on the
+    # way in 32 bits by a few of 2^-149, of which gamma < 2 makes at most twice as many
+    bound = (2.0 ** -8 + 2.0 ** -17) * want.abs() + 2.0 ** -134 + 2.0 ** -145
+    bad = ~((got - want).abs() <= bound)
+    there = (y != 0).any(-1)  # (a row without an entry left has no direction where eps is 0)
+    assert not bool(bad[there].any()), [(int(i), float(got[i, j]), float(want[i, j])) for i, j in bad.nonzero()[:5]]
