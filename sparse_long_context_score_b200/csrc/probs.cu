@@ -272,11 +272,11 @@ __global__ void __launch_bounds__(kThreads) probs_listed_kernel(const __grid_con
   const int e = blockIdx.x, parts = chunks + gridDim.x, b = b0 + blockIdx.y, j = blockIdx.z, V = a.V;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const size_t row = (size_t)b * a.S + j;
-  // The second of these kernels starts when all CTAs of the second pass are past their wait, which
-  // the lists and the partials are complete behind: it waits for that pass only before it writes,
-  // or ends (what comes behind it in the stream takes the pass for done, too).
+  // Nothing that a kernel before wrote is read ahead of the wait.  (The second of these kernels
+  // starts when all CTAs of the second pass are past theirs, which the lists and the partials are
+  // complete behind; but only its own wait makes them visible to it.)
+  sm100::grid_dep_wait();
   if constexpr (!kWrite) {
-    sm100::grid_dep_wait();
     sm100::grid_dep_launch();
   }
   const Listed* entry = lists.entries + (size_t)b * lists.room + kThreads * e + threadIdx.x;
@@ -287,8 +287,9 @@ __global__ void __launch_bounds__(kThreads) probs_listed_kernel(const __grid_con
   const RowSettings set = row_settings(a, b);
   const Partial none{-INFINITY, set.greedy ? kNoPlace : 0.f};
   if (!__syncthreads_or(there)) {  // nothing but gaps
-    if constexpr (kWrite) sm100::grid_dep_wait();
-    else if (threadIdx.x == 0) partials[row * parts + chunks + e] = none;
+    if constexpr (!kWrite) {
+      if (threadIdx.x == 0) partials[row * parts + chunks + e] = none;
+    }
     return;
   }
   float z = there ? load_f32(static_cast<const T*>(a.logits) + row * V + v) : -INFINITY;
@@ -320,7 +321,6 @@ __global__ void __launch_bounds__(kThreads) probs_listed_kernel(const __grid_con
       if (set.greedy) share = (float)v == x.s ? 1.f : 0.f;
       else share = (ordinary(x.m, set.c) ? exp2_approx((z - x.m) * set.c) : counts_as_one(z, x.m, set.c) ? 1.f : 0.f) / x.s;
     }
-    sm100::grid_dep_wait();
     if (there) a.p[row * V + v] = share;
   }
 }

@@ -393,3 +393,25 @@ def test_a_captured_verify_step_equals_the_calls_one_by_one(dsa):
         for x, y in zip(got[2:], want[2:]):
             assert torch.equal(x, y)
     assert dsa.dsa_check_device_status() == 0
+
+
+@pytest.mark.parametrize("B,S,V", [(16, 7, 20480), (40, 4, 5003), (37, 3, 325001)])
+def test_calls_in_a_row_share_a_workspace(dsa, B, S, V):
+    """Calls one right behind the other on one workspace, their lists, maxima and greedy rows all
+    different: none reads what the one before it left there."""
+    jobs = [_inputs(B, S, V, seed=30 + i, hist=(900, 40, 300)[i], bias=(0, 20, 7)[i], mask=i == 1, spread=True,
+                    greedy=((1,), (), (0, B - 1))[i]) for i in range(3)]
+    jobs[2]["logits"] += 50.0
+    alone = []
+    for a in jobs:
+        alone.append(dsa.dsa_logits_probs(**a))
+        torch.cuda.synchronize()
+    ws = torch.empty(max(dsa.lib().dsa_probs_workspace_size(B, S, V, 900, 20), 1), dtype=torch.uint8, device="cuda")
+    outs = [[torch.empty_like(p) for _ in range(2)] for p in alone]
+    for round_ in range(10):
+        ws.fill_(255 if round_ % 2 else 0)
+        for k in range(2):
+            for a, out in zip(jobs, outs):
+                dsa.dsa_logits_probs(**a, out=out[k], ws=ws)
+        for p, out in zip(alone, outs):
+            assert torch.equal(out[0], p) and torch.equal(out[1], p)
