@@ -7,6 +7,8 @@
 // layer reads the target cache -- KV Share).
 #include <cmath>
 #include <cstdio>
+#include <cstdlib>
+#include <initializer_list>
 #include <vector>
 
 #include "dsa.h"
@@ -46,6 +48,37 @@ inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_
 inline bool overlap(const void* p, size_t p_bytes, const void* q, size_t q_bytes) {
   const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
   return a < b ? b - a < p_bytes : a - b < q_bytes;
+}
+
+// Whether any of `outs` shares a byte with any of `ins` (null pointers: nothing).
+struct Range {
+  const void* p;
+  size_t bytes;
+};
+inline bool any_overlap(std::initializer_list<Range> outs, std::initializer_list<Range> ins) {
+  for (const Range& o : outs)
+    for (const Range& i : ins)
+      if (o.p && i.p && overlap(o.p, o.bytes, i.p, i.bytes)) return true;
+  return false;
+}
+
+// Whether [n][heads][dim] elements at x and others `shift` elements behind them, both with strides
+// `token` and `head`, have an element in common.  No two heads of one of them overlap, so along its
+// larger stride and then along its smaller one only the two nearest places can meet.
+inline bool views_meet(long long shift, long long n, long long heads, long long dim, long long token, long long head) {
+  if (n == 1) token = 0;
+  if (heads == 1) head = 0;
+  const bool tokens_out = token >= head;
+  const long long far = tokens_out ? token : head, near = tokens_out ? head : token;
+  const long long far_n = tokens_out ? n : heads, near_n = tokens_out ? heads : n;
+  if (shift < 0) shift = -shift;
+  for (long long i = far ? shift / far : 0, e = far ? i + 1 : 0; i <= e && i < far_n; ++i) {
+    long long rest = shift - i * far;
+    if (rest < 0) rest = -rest;
+    for (long long j = near ? rest / near : 0, f = near ? j + 1 : 0; j <= f && j < near_n; ++j)
+      if (std::llabs(rest - j * near) < dim) return true;
+  }
+  return false;
 }
 
 inline size_t round256(size_t b) { return (b + 255) & ~(size_t)255; }
@@ -570,6 +603,11 @@ dsa_status dsa_rope(const void* x, const long long* positions, long long n, int 
   const bool heads_out = (n <= 1 || out_token >= dim) && (heads == 1 || out_head >= (n - 1) * out_token + dim);
   if (!tokens_out && !heads_out) return DSA_ERR_INVALID_ARG;
   if (n == 0) return DSA_OK;
+  // (views of other strides than the output's are the caller's word)
+  const long long shift = (long long)(reinterpret_cast<intptr_t>(out) - reinterpret_cast<intptr_t>(x)) / (long long)esz;
+  if (x != out && (n == 1 || x_token == out_token) && (heads == 1 || x_head == out_head) &&
+      views_meet(shift, n, heads, dim, out_token, out_head))
+    return DSA_ERR_INVALID_ARG;
   return cuda_status(
       launch_rope(x, positions, n, heads, dim, rot_offset, *plan, dtype, x_token, x_head, out, out_token, out_head, stream));
 }
@@ -607,9 +645,13 @@ dsa_status dsa_paged_attn(const uint16_t* q, const uint16_t* cache, const int32_
   if (H > 128 || (long long)n * H > 0x7FFFFF00LL) return DSA_ERR_UNSUPPORTED;
   if (n == 0) return DSA_OK;
   const size_t rows = (size_t)n * H, pool = (size_t)num_pages * page_size * kDqk * 2;
-  if (overlap(out, rows * kDv * 2, q, rows * kDqk * 2) || overlap(out, rows * kDv * 2, cache, pool) ||
-      (lse && (overlap(lse, rows * 4, q, rows * kDqk * 2) || overlap(lse, rows * 4, cache, pool) ||
-               overlap(lse, rows * 4, out, rows * kDv * 2))))
+  const Range o{out, rows * kDv * 2}, l{lse, rows * 4};
+  if (any_overlap({o, l}, {{q, rows * kDqk * 2},
+                           {cache, pool},
+                           {table, (size_t)B * max_pages * 4},
+                           {cu_q, (B + (size_t)1) * 4},
+                           {ctx_len, (size_t)B * 4}}) ||
+      any_overlap({o}, {l}))
     return DSA_ERR_INVALID_ARG;
   const size_t need = paged_attn_workspace_bytes();
   if (need == 0) return cuda_status(cudaErrorInvalidDevice);
@@ -664,8 +706,20 @@ dsa_status dsa_logits_probs(const void* logits, int dtype, int B, int S, int V, 
   a.nbias = nbias;
   const size_t need = probs_workspace_bytes(B, S, V, history ? history_cap : 0, nbias);
   if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256))) return DSA_ERR_WORKSPACE;
-  const size_t entries = (size_t)B * S * V;
-  if (overlap(p, entries * 4, logits, entries * (dtype == DSA_F32 ? 4 : 2))) return DSA_ERR_INVALID_ARG;
+  const size_t entries = (size_t)B * S * V, each = (size_t)B * 4, biases = (size_t)B * nbias * 4;
+  if (any_overlap({{p, entries * 4}}, {{logits, entries * (dtype == DSA_F32 ? 4 : 2)},
+                                       {temperature, each},
+                                       {repetition, each},
+                                       {frequency, each},
+                                       {presence, each},
+                                       {a.history, (size_t)B * history_cap * 4},
+                                       {history_len, each},
+                                       {prompt_len, each},
+                                       {draft, (size_t)B * S * 4},
+                                       {nbias ? bias_ids : nullptr, biases},
+                                       {nbias ? bias_values : nullptr, biases},
+                                       {mask, (size_t)B * S * ((V + 31) / 32) * 4}}))
+    return DSA_ERR_INVALID_ARG;
   return cuda_status(launch_probs(a, workspace, stream));
 }
 

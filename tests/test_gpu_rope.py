@@ -297,3 +297,37 @@ def test_append_rows_of_any_magnitude(dsa, eps):
     bad = ~((got - want).abs() <= bound)
     there = (y != 0).any(-1)  # (a row without an entry left has no direction where eps is 0)
     assert not bool(bad[there].any()), [(int(i), float(got[i, j]), float(want[i, j])) for i, j in bad.nonzero()[:5]]
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_rope_between_views_of_one_buffer(dsa, layout):
+    """Same strides, any shift: refused where the two views share an element, right where they
+    lie between one another."""
+    import random
+    rng, plan, refused = random.Random(3), dsa.dsa_rope_init(8, layout), 0
+    for i in range(300):
+        n, heads, dim = rng.randint(1, 5), rng.randint(1, 4), rng.choice([8, 9, 16])
+        head = dim + rng.randint(0, 40)
+        token = (heads - 1) * head + dim + rng.randint(0, 90)
+        if i % 2:  # heads outermost
+            token = dim + rng.randint(0, 40)
+            head = (n - 1) * token + dim + rng.randint(0, 90)
+        shift = rng.randint(1, 400)
+        reach = (n - 1) * token + (heads - 1) * head + dim
+        buffer = torch.randn(reach + shift, generator=_gen(i), device="cuda")
+        at = [t * token + h * head + d for t in range(n) for h in range(heads) for d in range(dim)]
+        meet = bool(set(at) & {s + shift for s in at})
+        first, second = (buffer[k:].as_strided((n, heads, dim), (token, head, 1)) for k in (0, shift))
+        x, out = (first, second) if i % 3 else (second, first)
+        positions = torch.arange(n, device="cuda") * 1001
+        before, was = x.clone(), buffer.clone()
+        if meet:
+            refused += 1
+            with pytest.raises(dsa.DsaError):
+                dsa.dsa_rope(x, positions, plan, out=out)
+            assert torch.equal(buffer, was)
+        else:
+            dsa.dsa_rope(x, positions, plan, out=out)
+            _check_rope(before, out, positions, 0, 8, layout)
+            assert torch.equal(x, before)
+    assert 50 < refused < 250

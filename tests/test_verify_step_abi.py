@@ -170,3 +170,58 @@ def test_binding_refuses_cpu_tensors():
                            ws=torch.zeros(256, dtype=torch.uint8))
     with pytest.raises(ValueError):
         dsa.dsa_logits_probs(torch.zeros(1, 1, 32))
+
+
+def test_rope_refuses_views_that_meet(L):
+    """x and out as shifted views of one buffer, with the same strides (none of these calls may run)."""
+    plan = dsa.dsa_rope_init(64)
+    p = ctypes.addressof(plan)
+
+    def call(shift, n=4, heads=2, dim=64, token=128, head=64):
+        return L.dsa_rope(AT, FAKE, n, heads, dim, 0, p, 0, token, head, AT + 2 * shift, token, head, None)
+
+    for shift in (1, 63, 64, 65, 128, 3 * 128 + 127, -1, -64, -(3 * 128 + 127)):
+        assert call(shift) == -1, shift
+    for shift in (63, 192, 192 + 63, 192 * 9 - 63, -(192 * 9 + 63), 192 * 3 + 65 - 2):  # heads of wider rows
+        assert call(shift, n=10, heads=1, token=192, head=5) == -1, shift
+    for shift in (64 * 5, 1000 - 63, 1000 + 64 * 9 + 63, -(1000 - 64)):                  # heads outermost
+        assert call(shift, n=10, heads=2, token=64, head=1000) == -1, shift
+    assert call(64, n=1, heads=3, token=7) == -1 and call(2 * 64, n=1, heads=3, token=7) == -1
+
+
+def test_outputs_over_any_input_are_refused(L):
+    far = lambda i: AT + (i << 24)  # noqa: E731
+    names = ["q", "cache", "table", "cu", "ctx"]
+    size = dict(q=4 * 16 * 1152, cache=8 * 64 * 1152, table=2 * 4 * 4, cu=3 * 4, ctx=2 * 4)
+    out_size, lse_size = 4 * 16 * 1024, 4 * 16 * 4
+    a = {k: far(i) for i, k in enumerate(names)}
+
+    def attn(out, lse):
+        return L.dsa_paged_attn(a["q"], a["cache"], a["table"], a["cu"], a["ctx"], 4, 2, 16, 8, 64, 4, 0.1, out, lse, FAKE,
+                                1 << 40, None)
+
+    for k in names:
+        last = size[k] - size[k] % 16 - (16 if size[k] % 16 == 0 else 0)
+        for out in (a[k], a[k] + last, a[k] - out_size + 16):
+            assert attn(out, None) == -1, (k, out - a[k])
+        for lse in (a[k], a[k] + size[k] - 4, a[k] - lse_size + 4):
+            assert attn(far(9), lse) == -1, (k, lse - a[k])
+    assert attn(far(9), far(9) + out_size - 4) == -1 and attn(far(9), far(9) - lse_size + 4) == -1
+
+    # (sizes that take two passes, and so a workspace, on any device)
+    B, S, V, cap, nb = 400, 3, 5000, 10, 4
+    names = ["temperature", "repetition", "frequency", "presence", "history", "history_len", "prompt_len", "draft", "bias_ids",
+             "bias_values", "mask"]
+    size = dict.fromkeys(names, B * 4)
+    size.update(history=B * cap * 4, draft=B * S * 4, bias_ids=B * nb * 4, bias_values=B * nb * 4, mask=B * S * 157 * 4)
+    a = {k: far(2 * i + 2) for i, k in enumerate(names)}
+
+    def probs(p, **kw):
+        x = {**a, **kw}
+        return L.dsa_logits_probs(far(40), 1, B, S, V, x["temperature"], x["repetition"], x["frequency"], x["presence"],
+                                  x["history"], cap, x["history_len"], x["prompt_len"], x["draft"], x["bias_ids"],
+                                  x["bias_values"], nb, x["mask"], p, FAKE, 1 << 40, None)
+
+    for k in names:
+        for p in (a[k], a[k] + size[k] - 4, a[k] - B * S * V * 4 + 4):
+            assert probs(p) == -1, (k, p - a[k])
