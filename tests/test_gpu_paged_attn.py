@@ -4,7 +4,7 @@ import math
 import pytest
 import torch
 
-from verify_step import DQK, DV, Batch, attention, attention_bounds
+from verify_step import DQK, DV, Batch, attention, attention_bounds, marked_bounds
 
 pytestmark = pytest.mark.gpu
 SCALE = 1 / 24
@@ -432,3 +432,89 @@ def test_infinite_latents_that_some_queries_multiply_by_zero(dsa, ctx):
     b_out, b_lse = attention_bounds(*want, ctx)
     assert bool(((out[:, kind == 1].double() - want[0]).abs() <= b_out).all())
     assert bool(((lse[:, kind == 1].double() - want[1]).abs() <= b_lse).all())
+
+
+LONG = [
+    ([1], [65536], 16, 64),
+    ([1], [65499], 64, 128),
+    ([1, 1, 1], [40000, 23000, 129], 64, 16),
+    ([8, 3, 1], [30011, 52345, 900], 48, 64),
+    ([1], [262143], 16, 256),
+    ([200, 1], [33000, 128], 16, 48),
+    ([2] * 40, [1000 + 313 * i for i in range(40)], 64, 64),
+    ([5], [50001], 1, 32),
+    ([1] * 7, [9000] * 7, 128, 128),
+]
+
+
+def _marked(new, ctx, page, column, seed=0):
+    """A batch whose cached row at position s is zero but for a one in entry column(s)."""
+    batch = Batch(new, ctx, page, seed=seed)
+    flat = batch.cache.view(-1, DQK)
+    for b in range(len(new)):
+        r = batch.rows(b).cuda()
+        flat[r] = 0
+        flat[r, column(torch.arange(len(r), device="cuda"))] = 1
+    return batch
+
+
+def _tokens(batch):
+    """(token, sequence, cached rows that it sees) of each new token."""
+    for b, (new, ctx) in enumerate(zip(batch.new, batch.ctx)):
+        for t in range(new):
+            yield batch.ends[b] + t, b, ctx - new + t + 1
+
+
+@pytest.mark.parametrize("mark", ["tile", "place"])
+@pytest.mark.parametrize("new,ctx,heads,page", LONG)
+def test_every_cached_row_counts_once(dsa, new, ctx, heads, page, mark):
+    """Equal logits, the rows of a key tile (or those at the same place of all tiles) marked in an
+    entry of their own: each entry of the output is their part of the rows seen."""
+    column = (lambda s: s // 128 % DV) if mark == "tile" else (lambda s: s % 128 * 4 + s // 128 % 4)
+    batch = _marked(new, ctx, page, column)
+    q = torch.zeros((batch.n, heads, DQK), dtype=torch.bfloat16, device="cuda")
+    out, lse = dsa.dsa_paged_attn(q, batch.cache, batch.table, batch.cu_q, batch.ctx_len, SCALE)
+    at = column(torch.arange(max(ctx), device="cuda"))
+    want = torch.empty((batch.n, DV), dtype=torch.float64, device="cuda")
+    seen = torch.empty(batch.n, dtype=torch.float64, device="cuda")
+    for i, _, rows in _tokens(batch):
+        want[i], seen[i] = torch.bincount(at[:rows], minlength=DV) / rows, rows
+    b_out, b_lse = marked_bounds(want, seen.log())
+    assert bool(((out.double() - want[:, None]).abs() <= b_out[:, None]).all())
+    assert bool(((lse.double() - seen.log()[:, None]).abs() <= b_lse[:, None]).all())
+
+
+@pytest.mark.parametrize("shape", ["up", "down", "zigzag", "peaks"])
+@pytest.mark.parametrize("new,ctx,heads,page", LONG)
+def test_every_key_tile_has_its_weight(dsa, new, ctx, heads, page, shape):
+    """Key tiles marked as above, each at a logit of its own, so that maxima grow, fall, jump and are
+    guessed wrong; heads with other factors, two signs.  S is one exact product."""
+    batch = _marked(new, ctx, page, lambda s: s // 128 % DV)
+    tiles = (max(ctx) + 127) // 128
+    g = torch.Generator().manual_seed(tiles)
+    level = {"up": torch.linspace(0, 240, tiles).round(), "down": torch.linspace(240, 0, tiles).round(),
+             "zigzag": torch.randint(-80, 81, (tiles,), generator=g).float(),
+             "peaks": torch.where(torch.rand(tiles, generator=g) < 0.1, 160.0, 0.0)}[shape]
+    flat, entry, scale = batch.cache.view(-1, DQK), DV + 3, 0.125
+    for b in range(len(new)):
+        r = batch.rows(b)
+        flat[r.cuda(), entry] = level[torch.arange(len(r)) // 128].to(torch.bfloat16).cuda()
+    factor = torch.tensor([1.0, -1.0, 0.5, 2.0], dtype=torch.float64, device="cuda").repeat(32)[:heads]
+    q = torch.zeros((batch.n, heads, DQK), dtype=torch.bfloat16, device="cuda")
+    q[:, :, entry] = factor.to(torch.bfloat16)
+    out, lse = dsa.dsa_paged_attn(q, batch.cache, batch.table, batch.cu_q, batch.ctx_len, scale)
+    z = factor[:, None] * level.cuda().double() * scale                                # [heads, tiles], below 60
+    for i, _, rows in _tokens(batch):
+        count = (rows - 128 * torch.arange(tiles, device="cuda")).clamp(0, 128).double()
+        weight = z + count.log()
+        total = torch.logsumexp(weight, -1)
+        want = torch.zeros((heads, DV), dtype=torch.float64, device="cuda")
+        want.index_add_(1, torch.arange(tiles, device="cuda") % DV, (weight - total[:, None]).exp())
+        # The weights' and the output's roundings; in 32 bits, an exponent passes three roundings of
+        # up to 87 (in base 2) and an exponential (2^-22), once for its weight, for each of at most
+        # 87 / 8 moves of the maximum and for the join: 13 (3 x 87 x 2^-24 + 2^-22) < 2^-12
+        bound = (2.0 ** -7 + 2.0 ** -11) * want + 1e-36
+        assert bool(((out[i].double() - want).abs() <= bound).all()), i
+        assert bool(((lse[i].double() - total).abs() <= 2.0 ** -11).all()), i
+    assert dsa.dsa_check_device_status() == 0
+

@@ -6,7 +6,7 @@ import math
 import pytest
 
 import sparse_long_context_score_b200 as dsa
-from verify_step import frequencies
+from verify_step import DV, frequencies, marked_bounds
 
 FAKE = ctypes.c_void_p(1 << 20)  # aligned, never dereferenced: every call below fails validation
 AT = 1 << 20
@@ -225,3 +225,17 @@ def test_outputs_over_any_input_are_refused(L):
     for k in names:
         for p in (a[k], a[k] + size[k] - 4, a[k] - B * S * V * 4 + 4):
             assert probs(p) == -1, (k, p - a[k])
+
+
+@pytest.mark.parametrize("ctx,lost", [(900, 1), (65499, 1), (65536, 1), (65536, -1), (65536, 128), (65536, -128), (262143, 128),
+                                      (262143, -128)])
+def test_marked_rows_show_what_is_lost_or_taken_twice(ctx, lost):
+    """Planted mistakes: one row, or one key tile of 128, is left out or counts twice.  The bounds that
+    equal logits over marked rows are held to see it, in the output and in the log-sum-exp."""
+    import torch
+    count = torch.bincount(torch.arange(ctx) // 128 % DV, minlength=DV).double()
+    b_out, b_lse = marked_bounds(count / ctx, torch.tensor(ctx, dtype=torch.float64).log())
+    wrong = count.clone()
+    wrong[ctx // 2 // 128 % DV] -= lost
+    assert bool(((wrong / wrong.sum() - count / ctx).abs() > b_out).any())
+    assert abs(math.log(ctx - lost) - math.log(ctx)) > float(b_lse)

@@ -111,6 +111,14 @@ def attention_bounds(out, lse, size, reach, most):
     return 2.0 ** -8 * out.abs() + 1.01 * weight[..., None] * size + 1e-30, dz + (most + 8) * 2.0 ** -24 + 2.0 ** -22 * lse.abs()
 
 
+def marked_bounds(out, lse):
+    """How far (out, lse) may be where all logits are zero and values zero or one.  Weights of one
+    and their sums are exact in 32 bits; left are the quotient (2^-24), the product (2^-24) and the
+    output's rounding (2^-8), and of lse a logarithm (one unit), its product with ln 2 and that
+    constant (2^-21 in all)."""
+    return (2.0 ** -8 + 2.0 ** -22) * out, 2.0 ** -21 * lse + 2.0 ** -40
+
+
 def probabilities(logits, temperature=None, history=None, history_len=None, prompt_len=None, draft=None, repetition=None,
                   frequency=None, presence=None, bias_ids=None, bias_values=None, mask=None):
     """(p, size) in 64 bits, on the CPU: size[b, j] the largest magnitude that a finite logit
