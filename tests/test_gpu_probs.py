@@ -415,3 +415,50 @@ def test_calls_in_a_row_share_a_workspace(dsa, B, S, V):
                 dsa.dsa_logits_probs(**a, out=out[k], ws=ws)
         for p, out in zip(alone, outs):
             assert torch.equal(out[0], p) and torch.equal(out[1], p)
+
+
+@pytest.mark.parametrize("B,V", [(1, 3000), (1, 50000), (1, 400000), (200, 3000)])
+def test_large_counts_move_the_probability(dsa, B, V):
+    """A token said thousands of times whose adjusted logit, 6.5, is near the largest, 8: one count
+    more or less moves its probability by 28%.  All values are exact in 32 bits."""
+    L = 5000
+    z = torch.zeros((B, 3, V), device="cuda")
+    z[..., 17], z[..., 18] = 2464.0, 16.0
+    history = torch.full((B, L), 17, dtype=torch.int32, device="cuda")
+    history[:, :100] = 18
+    full = lambda x, dtype=torch.float32: torch.full((B,), x, dtype=dtype, device="cuda")  # noqa: E731
+    got = dsa.dsa_logits_probs(
+        z, history=history, prompt_len=full(100, torch.int32), draft=torch.tensor([[17, 9, 9]], device="cuda").int().repeat(B, 1),
+        repetition=full(2.0), frequency=full(0.25), presence=full(1.0),
+        bias_ids=torch.tensor([[17]], device="cuda").int().repeat(B, 1), bias_values=full(0.5)[:, None]).double()
+    for j, count in enumerate([4900, 4901, 4901]):  # (the first draft counts in the rows behind it)
+        want = torch.zeros(V, dtype=torch.float64, device="cuda")
+        want[17], want[18] = 1232 - 0.25 * count - 1 + 0.5, 8.0
+        if j == 2:
+            want[9] = -0.25 - 1
+        want = torch.softmax(want, -1)
+        # exact logits; a product with log2 e, an exponential, a sum of at most 400000 terms (fewer
+        # than 1024 additions deep) and a quotient: under 2^-13
+        assert float(want[17]) > 1e-4 and bool(((got[:, j] - want).abs() <= 2.0 ** -13 * want).all())
+
+
+def test_workspace_refusals_on_a_device(dsa):
+    """Many rows need their workspace, whole and aligned; few rows need none."""
+    z = torch.zeros((400, 3, 5000), device="cuda")
+    size = dsa.lib().dsa_probs_workspace_size(400, 3, 5000, 0, 0)
+    assert size > 0
+    room = torch.empty(size + 256, dtype=torch.uint8, device="cuda")
+    for ws in (room[:size - 1], room[16:16 + size], room[:0]):
+        with pytest.raises(dsa.DsaError) as err:
+            dsa.dsa_logits_probs(z, ws=ws)
+        assert err.value.status == -3
+    p = dsa.dsa_logits_probs(z, ws=room[:size])
+    assert bool(((p.double() - 1 / 5000).abs() <= 2.0 ** -20 / 5000).all())
+    assert dsa.lib().dsa_probs_workspace_size(2, 3, 100, 0, 0) == 0
+    few, p = torch.zeros((2, 3, 100), device="cuda"), torch.empty((2, 3, 100), device="cuda")
+    none = [None] * 5
+    rc = dsa.lib().dsa_logits_probs(few.data_ptr(), 1, 2, 3, 100, *none, 0, None, None, None, None, None, 0, None, p.data_ptr(),
+                                    None, 0, torch.cuda.current_stream().cuda_stream)
+    assert rc == 0
+    torch.cuda.synchronize()
+    assert bool(((p.double() - 0.01).abs() <= 2.0 ** -20 * 0.01).all())

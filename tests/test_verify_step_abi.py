@@ -239,3 +239,19 @@ def test_marked_rows_show_what_is_lost_or_taken_twice(ctx, lost):
     wrong[ctx // 2 // 128 % DV] -= lost
     assert bool(((wrong / wrong.sum() - count / ctx).abs() > b_out).any())
     assert abs(math.log(ctx - lost) - math.log(ctx)) > float(b_lse)
+
+
+def test_logits_probs_workspace_refusals_on_any_machine(L):
+    """Sizes that take two passes whatever the number of SMs, outputs apart from the logits."""
+    B, S, V, cap, nb = 400, 3, 5000, 700, 4
+    need, more = L.dsa_probs_workspace_size(B, S, V, 0, 0), L.dsa_probs_workspace_size(B, S, V, cap, nb)
+    assert 0 < need < more
+
+    def call(ws, size, lists):
+        history, bias = (AT + (1 << 28), AT + (1 << 29)) if lists else (None, None)
+        return L.dsa_logits_probs(AT, 1, B, S, V, None, None, None, None, history, cap if lists else 0, None, None, None, bias,
+                                  bias, nb if lists else 0, None, AT + (1 << 26), ws, size, None)
+
+    for lists, size in ((False, need), (True, more)):
+        for ws, n in ((None, size), (AT, size - 1), (AT, 0), (AT + 16, size)):
+            assert call(ws, n, lists) == -3
