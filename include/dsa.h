@@ -443,7 +443,9 @@ dsa_status dsa_cache_append(const uint16_t *x, long long x_stride, const uint16_
  * bf16 operands (the weights are rounded to bf16 before the product with the values), f32
  * accumulation and softmax, one rounding of the output.  Rows behind ctx_len[b] may hold
  * anything, NaN included, and a cached row that is not finite concerns only the tokens that see
- * it: a logit of NaN or +inf makes a token's row of out and lse NaN, one of -inf weighs nothing.
+ * it: a logit of NaN or +inf makes a token's row of out and lse NaN, one of -inf weighs nothing,
+ * whatever the row's values.  Logits are held in base 2: one above 2e38 counts as +inf, one below
+ * -2e38 as -inf.
  * workspace: dsa_paged_workspace_size(n, B, H) bytes, 256-byte aligned, written by every call
  * (calls that overlap on the GPU need one each); the size depends on the current device.
  * out and lse must not overlap an input or each other.

@@ -131,8 +131,14 @@ constexpr int kPartFloats = kRows * kDv;             // one part's [64][512] sum
 
 constexpr float kRescaleFactor = 256.f;  // 2^kRescaleLog2
 // The maximum that weights are taken from before a row has one: a logit of minus infinity weighs
-// nothing (from -inf it would be NaN), any other one too much, so that a guess is taken back.
+// nothing (from -inf it would be NaN), any other one too much, so that a guess is taken back.  (What
+// lies below it, -2.08e38 in base e, counts as minus infinity.)
 constexpr float kNoMax = -3e38f;
+// A weight is 2^(scale z - m), m the rounded scale z of the row's maximum, and one fused operation
+// does not round scale z: what the two differ by, up to 2^-24 |m|, is common to the row and cancels,
+// but from some 2^31 on it takes the largest weight itself out of range.  From this size of a tile's
+// maximum on, every product is rounded on its own, as m was.
+constexpr float kLargeMax = 65536.f;
 
 // 2^x; results below the normal range become zero
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -548,7 +554,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
       for (int r = 0; r < 32; ++r) {
         l[r] = 0.f;
       }
-      bool guessed = false;
+      bool guessed = false, large = false;
       const int count = s.k1 - s.k0;
       for (int next = 0; next < count;) {
         ok = warp_wait(sfull_bar, sp & 1, 51);
@@ -561,7 +567,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
         // segment's first and last tiles do.
         const bool redo = guessed && *s_over == tiles;
         const int n = redo ? next - 1 : next, k = tile_at(s, n);
-        const bool exchange = redo || n == 0 || n + 1 == count;
+        const bool exchange = redo || n == 0 || n + 1 == count || large;
         if (!redo) ++tiles;
         const uint32_t bad = *s_bad;
         uint32_t z[32];
@@ -594,15 +600,20 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
           float mine = -INFINITY;  // of row 32 half + lane over the warp's keys
 #pragma unroll
           for (int r = 0; r < 32; ++r) {
-            const float t = warp_max(r >= from ? __uint_as_float(z[r]) * scale_log2 : -INFINITY);
+            const float t = warp_max(r >= from ? __fmul_rn(__uint_as_float(z[r]), scale_log2) : -INFINITY);
             if (lane == r) mine = t;
           }
           s_max[64 * quarter + 32 * half + lane] = mine;
           ok = group_sync(52);
           if (!ok) break;
-          float t = -INFINITY;
+          float t = -INFINITY, other = -INFINITY;  // of the other half's rows, so that all warps agree on `large`
 #pragma unroll
-          for (int q = 0; q < 4; ++q) t = fmaxf(t, s_max[64 * q + 32 * half + lane]);
+          for (int q = 0; q < 4; ++q) {
+            t = fmaxf(t, s_max[64 * q + 32 * half + lane]);
+            other = fmaxf(other, s_max[64 * q + 32 * (half ^ 1) + lane]);
+          }
+          auto far = [](float x) { return fabsf(x) > kLargeMax && fabsf(x) < INFINITY; };
+          large = large || __any_sync(0xFFFFFFFFu, far(t) || far(other));
           float alpha = 1.f;
           if (mrow == -INFINITY) {
             mrow = t;
@@ -618,6 +629,14 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
           if (scaled) {
 #pragma unroll
             for (int r = 0; r < 32; ++r) l[r] *= __shfl_sync(0xFFFFFFFFu, alpha, r);
+          }
+          if (large) {  // `weight` takes what is left of each exponent (all tiles of the segment come here from now on)
+            const float back = 1.f / scale_log2;
+#pragma unroll
+            for (int r = 0; r < 32; ++r) {
+              z[r] = __float_as_uint((__fmul_rn(__uint_as_float(z[r]), scale_log2) - m[r]) * back);
+              m[r] = 0.f;
+            }
           }
           if (n > 0) {
             if (quarter == 0) {

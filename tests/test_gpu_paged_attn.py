@@ -518,3 +518,57 @@ def test_every_key_tile_has_its_weight(dsa, new, ctx, heads, page, shape):
         assert bool(((lse[i].double() - total).abs() <= 2.0 ** -11).all()), i
     assert dsa.dsa_check_device_status() == 0
 
+
+
+@pytest.mark.parametrize("ctx", [5, 128, 3000, 40000])
+@pytest.mark.parametrize("logit,counts", [(-1.9e38, True), (1.9e38, True), (-2.2e38, False), (-3.3e38, False)])
+def test_logits_at_the_ends_of_their_range(dsa, ctx, logit, counts):
+    """All rows as if masked by a number that large: equal weights up to 2e38; below -2e38 a row of
+    nothing."""
+    batch = Batch([1], [ctx], 64).fill()
+    entry = torch.tensor(logit).to(torch.bfloat16)
+    flat, r = batch.cache.view(-1, DQK), batch.rows(0).cuda()
+    flat[r, DV:] = 0
+    flat[r, DV] = entry.cuda()
+    q = torch.zeros((1, 16, DQK), dtype=torch.bfloat16, device="cuda")
+    q[..., DV] = 1
+    out, lse = dsa.dsa_paged_attn(q, batch.cache, batch.table, batch.cu_q, batch.ctx_len, 1.0)
+    if not counts:
+        assert bool((out == 0).all()) and bool((lse == -math.inf).all())
+        return
+    rows = flat[r, :DV].double()
+    assert bool(((out.double() - rows.mean(0)).abs() <= 2.0 ** -8 * rows.mean(0).abs() + ctx * 2.0 ** -24 * rows.abs().mean(0)).all())
+    # base 2 and back: four roundings
+    assert bool(((lse.double() - float(entry)).abs() <= 2.0 ** -22 * abs(float(entry))).all())
+
+
+@pytest.mark.parametrize("new,ctx,heads", [([1], [100], 16), ([1, 3], [3000, 129], 64), ([1], [40000], 16), ([4] * 48, [2300] * 48, 64)])
+@pytest.mark.parametrize("logit", [1e5, 3e7, 1e9, 1e10, 1e20, 1.9e38, -1e5, -3e7, -1e9, -1e10, -1e20, -1.9e38])
+def test_huge_logits_share_what_the_largest_have(dsa, new, ctx, heads, logit):
+    """Logits of one size, some rows' a step of bf16 above the others': those share the weight."""
+    batch = Batch(new, ctx, 64, seed=3).fill(seed=3)
+    low = torch.tensor(logit).to(torch.bfloat16)
+    bits = low.view(torch.int16)
+    high = (bits - 1 if logit < 0 else bits + 1).view(torch.bfloat16)  # the next one above
+    flat, scale = batch.cache.view(-1, DQK), 1.0
+    q = torch.zeros((batch.n, heads, DQK), dtype=torch.bfloat16, device="cuda")
+    q[..., DV] = 1
+    g, best = torch.Generator().manual_seed(4), []
+    for b in range(len(new)):
+        r = batch.rows(b)
+        top = torch.rand(len(r), generator=g) < 0.05
+        top[:1 + len(r) // 2] &= b % 2 == 0            # (not before the middle of every other context)
+        flat[r.cuda(), DV:] = 0
+        flat[r.cuda(), DV] = torch.where(top, high, low).cuda()
+        best.append(top)
+    out, lse = dsa.dsa_paged_attn(q, batch.cache, batch.table, batch.cu_q, batch.ctx_len, scale)
+    for i, b, seen in _tokens(batch):
+        top = best[b][:seen]
+        top = top if top.any() else ~top
+        rows = flat[batch.rows(b)[:seen][top].cuda(), :DV].double()
+        value = float(high if best[b][:seen].any() else low)
+        # weights of one among themselves; the next ones' are e^(-2^-8 10^5) at most
+        bound = 2.0 ** -8 * rows.mean(0).abs() + (2.0 ** -8 + len(rows) * 2.0 ** -23) * rows.abs().mean(0) + 1e-30
+        assert bool(((out[i].double() - rows.mean(0)).abs() <= bound).all()), i
+        # base 2 and back: four roundings of that size
+        assert bool(((lse[i].double() - value - math.log(len(rows))).abs() <= 2.0 ** -21 * abs(value)).all()), i
