@@ -462,3 +462,37 @@ def test_workspace_refusals_on_a_device(dsa):
     assert rc == 0
     torch.cuda.synchronize()
     assert bool(((p.double() - 0.01).abs() <= 2.0 ** -20 * 0.01).all())
+
+
+@pytest.mark.parametrize("B,S,V", [(2, 1, 50257), (3, 2, 151552), (60, 4, 5003)])
+@pytest.mark.parametrize("cap,told", [(200_000, 200_000), (1 << 20, 1000)])
+def test_long_histories(dsa, B, S, V, cap, told):
+    """Histories of a long context: all of it counts, or a thousand tokens of much room."""
+    g = _gen(cap + V)
+    history = torch.full((B, cap), -7, dtype=torch.int32, device="cuda")
+    history[:, :told] = torch.randint(0, V, (B, told), generator=g, device="cuda", dtype=torch.int32)
+    history[0, told // 2:told] = 11                              # one token very often
+    history[:, told:told + 50] = 3                               # behind the length: not told
+    lens = torch.full((B,), told, dtype=torch.int32, device="cuda")
+    lens[B - 1] = told - 7
+    prompt = torch.full((B,), told // 3, dtype=torch.int32, device="cuda")
+    draft = torch.randint(0, V, (B, S), generator=g, device="cuda", dtype=torch.int32)
+    z = torch.randn((B, S, V), generator=g, device="cuda") * 3
+    full = lambda x: torch.full((B,), x, device="cuda")  # noqa: E731
+    rep, freq, pres, T = full(1.25), full(0.125), full(0.5), full(0.75)
+    got = dsa.dsa_logits_probs(z, T, history=history, history_len=lens, prompt_len=prompt, draft=draft, repetition=rep,
+                               frequency=freq, presence=pres)
+    for b in range(B):
+        for j in range(S):
+            heard = history[b, :int(lens[b])].long()
+            said = torch.cat((heard[int(prompt[b]):], draft[b, :j].long()))
+            count = torch.bincount(said, minlength=V).double()
+            seen = (torch.bincount(heard, minlength=V) + count) > 0
+            y = z[b, j].double()
+            y = torch.where(seen, torch.where(y > 0, y / 1.25, y * 1.25), y) - 0.125 * count - 0.5 * (count > 0)
+            want = torch.softmax(y / 0.75, -1)
+            # an adjusted logit passes three roundings of values up to 2^7 for what is not negligible
+            # (p > 1e-30: y within 60 of the largest), and the temperature's and the exponent's
+            keep = want > 1e-30
+            assert bool(((got[b, j].double() - want).abs() <= 2.0 ** -12 * want)[keep].all())
+            assert float(got[b, j].double()[~keep].sum()) < 1e-20
