@@ -17,7 +17,7 @@
 // about the same time, and the shares' borders shift from tile to tile.  So every CTA starts where
 // its key tile's number is a multiple of the share's length, and takes the ones before that
 // last: at any time the CTAs of a sequence are at the same few places (16 sequences of 2 to 8 new
-// tokens x 64 heads over 4K to 32K: 1.29 -> 0.73 GB from HBM, 371 -> 351 us).  (Prefetching two
+// tokens x 64 heads over 4K to 32K: 1.29 -> 0.72 GB from HBM, 371 -> 351 us).  (Prefetching two
 // key tiles ahead into L2 on top of that gained 3 to 6% in short bursts of such calls, and lost 2 to
 // 4% of decode and of many sequences once the power limit is met.)
 //
@@ -27,7 +27,7 @@
 // The tile (147.5 KB) fills the rest of shared memory as nine blocks of 64 columns, and
 // there is no second one: S takes the blocks as they arrive, and each quarter of PV gives
 // two of them back, so the next tile's loads run behind PV and the next S behind the loads.
-// What bounds it: 512 query tokens x 64 heads x 2 over 16K take 5.32K cycles a key tile, 27.7
+// What bounds it: 512 query tokens x 64 heads x 2 over 16K take 5.37K cycles a key tile, 27.5
 // bytes a cycle into each SM of the 29.5 that all SMs at once get out of L2 (S 1.73K and PV 1.54K
 // cycles of MMAs, the softmax 1.32K).  8 tokens over 128K each: 7.0K cycles a key tile, HBM.
 // Keys on the M side: an MMA of M = 128, N = 64, K = 16 takes 48 cycles (its operands'
@@ -64,8 +64,8 @@ constexpr int kThreadsP = kSoftmaxWarp0 * 32 + kSoftmaxThreads;  // 384
 constexpr float kRescaleLog2 = 8.f;
 // Beginning a query tile costs a CTA as much as so many key tiles: the end of the one before
 // (maxima, sums, 131 KB of values) and a first key tile that nothing runs ahead of take 10K cycles
-// more than the 5.4K of a key tile.  Shares of equal key tiles: 16 verify chunks 340 us instead of
-// 330, 8 x 128K 251 instead of 248 (a prefill chunk 2730 instead of 2737).
+// more than the 5.4K of a key tile.  Shares of equal key tiles: 16 verify chunks 360 us instead of
+// 351, 8 x 128K 266 instead of 265 (a prefill chunk 2754 instead of 2757).
 constexpr int kTileCost = 2;
 
 // One CTA's part of a query tile.

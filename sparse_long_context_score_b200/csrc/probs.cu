@@ -18,7 +18,7 @@
 // stream by a bit each; a kernel behind it adds their share to the row's sums, and one behind the
 // second pass puts their probabilities over what that wrote there, a thread an entry.
 // 16 x 7 rows of 151552 (68 MB of logits, 68 MB of p), us, without lists / with 4096 tokens of
-// history, 32 biases and a mask: 34 / 55.  Tried: a row held in the registers of a cluster of
+// history, 32 biases and a mask: 34 / 56.  Tried: a row held in the registers of a cluster of
 // eight CTAs, one pass (83 / 133: one such CTA fills an SM, and its loads, lists, exchanges and
 // stores follow one another); lists as a number and a bit for every entry (34 / 82: a warp does
 // the repetition's arithmetic wherever one of its lanes needs it); the listed entries treated by

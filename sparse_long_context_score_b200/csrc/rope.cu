@@ -81,7 +81,8 @@ struct RopeArgs {
 // them, while the loads are in flight, and shared.
 // 4096 tokens, 67 MB read and written: 64 heads x 64 interleaved in views of wider rows, and
 // 32 heads x 128 of which 64 rotate in the half layout; a plain copy of the latter takes
-// 14.5 us.  17.0 and 15.5 us (with every thread computing its own angles, 16.9 and 18.8).
+// 14.5 us.  16.4 and 14.4 us; in 32 bits 25.0 and 23.5 us (134 MB; the copy 24.7).  (With every thread
+// computing its own angles the second took 3.3 us more, the first as long.)
 template <class T, int kHeads, bool kHalf>
 __global__ void __launch_bounds__(256) rope_wide_kernel(RopeArgs a, const __grid_constant__ dsa_rope_plan plan, int places,
                                                         int turned) {
@@ -203,7 +204,7 @@ __device__ __forceinline__ int find_sequence(const PagedBatch& p, int token, int
 // One warp per token: lane l holds latent entries 8 l .. 8 l + 7 and 256 + 8 l .. 256 + 8 l + 7
 // and the angle of rotary pair l; lanes 0 .. 7 hold the rotary part's eight chunks and take the
 // angles (in the half layout also the other ends) from the lanes that have them.  The row is
-// loaded before its place is looked up.  16 chunks of up to 8 tokens take 2.6 us, 10.9K tokens 7.8 us
+// loaded before its place is looked up.  16 chunks of up to 8 tokens take 2.6 us, 10.9K tokens 7.9 us
 // (3.2 TB/s): the chain of loads from the lengths over the table to the row's place.
 constexpr int kAppendWarps = 4;
 __global__ void __launch_bounds__(32 * kAppendWarps) append_kernel(const uint16_t* __restrict__ x, long long x_stride,
