@@ -572,3 +572,40 @@ def test_huge_logits_share_what_the_largest_have(dsa, new, ctx, heads, logit):
         assert bool(((out[i].double() - rows.mean(0)).abs() <= bound).all()), i
         # base 2 and back: four roundings of that size
         assert bool(((lse[i].double() - value - math.log(len(rows))).abs() <= 2.0 ** -21 * abs(value)).all()), i
+
+
+@pytest.mark.parametrize("scale", [SCALE, -SCALE])
+@pytest.mark.parametrize("size", [1e7, 1e12, 1e30])
+@pytest.mark.parametrize("shape", ["chunks", "one long"])
+def test_huge_logits_among_ordinary_ones(dsa, shape, size, scale):
+    """Whole key tiles and single rows far below and, for some heads, far above the rest, from the
+    middle of the contexts on: heads without one above weigh the ordinary rows as ever, the others'
+    largest ones share all of the weight."""
+    batch = _long_batch(False, 31) if shape == "chunks" else Batch([2], [40000], 64, seed=31).fill(seed=31)
+    q = _queries(batch.n, 64)
+    kind = torch.arange(64, device="cuda") % 3  # 0: no huge logit, 1: above, 2: below
+    q[:, :, DV + 1] = torch.where(kind == 0, 0.0, torch.where(kind == 1, 1.0, -1.0)).to(torch.bfloat16) * (1 if scale > 0 else -1)
+    flat, gone = batch.cache.view(-1, DQK), {}
+    for b, ctx in enumerate(batch.ctx):
+        r = batch.rows(b)
+        start = ctx // 2 + 7 * (b % 20)
+        gone[b] = torch.tensor(sorted(set(range(start, start + 300)) | {start + 511, ctx - 200, ctx - 99}))
+        flat[r.cuda(), DV + 1] = 0
+        flat[r[gone[b]].cuda(), DV + 1] = size
+        flat[r[gone[b]].cuda(), DV + 2:] = 0    # (the huge product alone)
+        flat[r[gone[b]].cuda(), DV] = 0
+    out, lse = dsa.dsa_paged_attn(q, batch.cache, batch.table, batch.cu_q, batch.ctx_len, scale)
+    assert dsa.dsa_check_device_status() == 0
+    for k, left_out in ((0, {b: torch.tensor([], dtype=torch.int64) for b in gone}), (2, gone)):
+        part = q[:, kind == k].contiguous()
+        want = attention(_Without(batch, left_out), part, scale)
+        b_out, b_lse = attention_bounds(*want, max(batch.ctx))
+        assert bool(((out[:, kind == k].double() - want[0]).abs() <= b_out).all()), k
+        assert bool(((lse[:, kind == k].double() - want[1]).abs() <= b_lse).all()), k
+    # above: which of the huge rows is largest depends on what 32 bits leave of the latent part beside
+    # the huge product, so only that no other row counts is told here
+    top = float(torch.tensor(size).to(torch.bfloat16)) * abs(scale)
+    assert bool(((lse[:, kind == 1].double() - top).abs() <= 2.0 ** -20 * top + 100).all())
+    most = max(float(flat[batch.rows(b)[gone[b]].cuda(), :DV].double().abs().max()) for b in gone)
+    assert bool((out[:, kind == 1].double().abs() <= most * (1 + 2.0 ** -7)).all()) and bool(out.isfinite().all())
+    assert bool((out[:, kind == 1].double().abs().amax(-1) > 0).all())
